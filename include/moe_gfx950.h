@@ -42,6 +42,13 @@
  *                  dequantisation scale per expert and matrix; x and h are
  *                  quantised to e4m3 inside the layer with dynamic
  *                  per-tensor scales (amax / 448).
+ *   MOE_INT8     : x, h, out bf16; w13, w2 int8 codes with one fp32 scale per
+ *                  expert and output channel (w13_scale [E,2I], w2_scale
+ *                  [E,H]); x and h are quantised to int8 inside the layer with
+ *                  one dynamic scale per row (moe_act_quant_i8); the products
+ *                  of codes are summed exactly in 32-bit integers.  H and I
+ *                  are at most 131072 in this mode (MOE_ERR_UNSUPPORTED), so
+ *                  that no such sum overflows.
  * Layouts (row-major, last index contiguous):
  *   x [T,H]; logits [T,E] fp32; w13 [E,2I,H] (rows 0..I-1 gate, I..2I-1 up);
  *   w2 [E,H,I]; h [T*k,I] and y [T*k,H] in expert-sorted pair order;
@@ -58,12 +65,12 @@
 extern "C" {
 #endif
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_INT8 = 4 } moe_dtype;
 
 typedef enum {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = -1, /* null / misaligned pointer, bad T, E, k, dtype */
-  MOE_ERR_UNSUPPORTED = -2, /* H or I not a multiple of 128 */
+  MOE_ERR_UNSUPPORTED = -2, /* H or I not a multiple of 128, or too long for int8 */
   MOE_ERR_WORKSPACE = -3,   /* workspace missing or smaller than required */
   MOE_ERR_HIP = -4,         /* a kernel launch failed */
   MOE_ERR_TOO_LARGE = -5    /* beyond moe_fused_forward_noalloc's scratch */
@@ -165,10 +172,13 @@ int moe_align_sort(const int32_t* topk_ids, int32_t T, int32_t k, int32_t E,
  *   FP8: x is first quantised per tensor (codes e4m3(x * 448/amax(x))), the
  *        products use the codes and both sums are scaled by
  *        fl32(s_x * w13_scale[e]), s_x = amax(x)/448.
+ *   INT8: x is first quantised row by row (moe_act_quant_i8); the integer
+ *        sum of row n is scaled by fl32(s_x[t] * w13_scale[e][n]).
  *   h[p][n] = silu(g_n) * u_n, stored in the activation type.
  * act_scales [4] fp32 out (FP8 mode; left untouched otherwise):
  *   {s_x, s_h, amax(x), amax(h)} with s_h = amax(h)/448 (amax = 0 -> scale 1).
- * w13_scale [E] is required in FP8 mode and ignored otherwise. */
+ * w13_scale is required in FP8 mode ([E]) and INT8 mode ([E,2I], in the row
+ * order of w13), ignored otherwise; act_scales may be NULL outside FP8. */
 int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w13,
                                 const float* w13_scale, const int32_t* sorted_ids,
                                 const int32_t* expert_offsets, void* h, float* act_scales,
@@ -182,14 +192,16 @@ int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w
  * Backend routing": scaling and matmul not as discrete steps).
  * h is in sorted order, so the position p alone names its expert (through
  * expert_offsets); no sorted_ids argument is needed.
- * h [T*k,I] activation type in, sorted order; w2 [E,H,I]; w2_scale [E] fp32
- * (FP8 only); act_scales [4] fp32 in as written by
+ * h [T*k,I] activation type in, sorted order; w2 [E,H,I]; w2_scale fp32 ([E]
+ * in FP8 mode, [E,H] in INT8 mode, else ignored); act_scales [4] fp32 in as written by
  * moe_grouped_gemm_w13_swiglu (FP8 only; only act_scales[3] is read);
  * ws / ws_bytes as for moe_workspace_bytes(s).
  *   y[p][m] = h[p] . w2[e][m] (fp32 accumulation), e the expert of position p.
  *   FP8: h is quantised per tensor with the scale derived from
  *        act_scales[3] = amax(h) (codes e4m3(h * 448/amax)), and y is scaled
  *        by fl32(s_h * w2_scale[e]).
+ *   INT8: h is quantised row by row (moe_act_quant_i8), and the integer sum
+ *        is scaled by fl32(s_h[p] * w2_scale[e][m]).
  * y [T*k,H] fp32 out, sorted order. */
 int moe_grouped_gemm_w2(const moe_shape* s, const void* h, const void* w2, const float* w2_scale,
                         const int32_t* expert_offsets, const float* act_scales, float* y,
@@ -222,6 +234,84 @@ int moe_combine(const moe_shape* s, const float* y, const int32_t* inv_perm,
  * not a positive multiple of 8, give MOE_ERR_INVALID_ARG; n = 0 returns
  * MOE_OK with nothing enqueued. */
 int moe_act_quant_e4m3(const void* a, int64_t n, uint8_t* codes, float* scales, void* stream);
+
+/* Dynamic per-row int8 quantisation of an activation, the step the INT8 mode
+ * applies to x before the gate/up projection (a row per token) and to h
+ * before the down projection (a row per pair).
+ *   a      [rows, n] bf16 in, n a positive multiple of 8
+ *   codes  [rows, n] int8 out: 127 a / amax rounded to the nearest integer,
+ *          ties to even, amax = max |a| over the row; the quotient is not
+ *          rounded before that, so the codes lie in [-127, 127]
+ *   scales [rows] fp32 out: fl32(amax / 127), the value of one code
+ *          (amax = 0: scale 1, codes 0)
+ * a holds no NaN and no infinity (precondition).  Null or misaligned (16 B)
+ * pointers, rows < 0 or >= 2^31, or n not a positive multiple of 8, give
+ * MOE_ERR_INVALID_ARG; rows = 0 returns MOE_OK with nothing enqueued. */
+int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, float* scales,
+                     void* stream);
+
+/* Load-balance loss of the router with its per-expert counts, for training
+ * the router that feeds moe_topk_gating.
+ *   logits      [T,E] fp32 in; topk_ids [T,k] int32 in (as moe_topk_gating
+ *               chose them; an id outside [0, E) is a dropped pair and is not
+ *               counted)
+ *   token_mask  [T] bytes in, 0 = the token does not count (padding); nothing
+ *               else of such a token is read.  NULL = every token counts
+ *   loss          [1] fp32 out: coef * E * sum_e f_e P_e with f_e =
+ *                 expert_counts[e] / (N k) and P_e = expert_probs[e]
+ *   expert_counts [E] int32 out: counted pairs routed to expert e
+ *   expert_probs  [E] fp32 out: the mean over the N counted tokens of
+ *                 softmax(logits)_e
+ *   token_count   [1] int32 out: N
+ *   ws, ws_bytes  workspace of moe_balance_loss_workspace_bytes, 256-byte
+ *                 aligned; holds nothing after the call
+ * A NaN logit is read as -inf (as the gating does), and a row without a
+ * finite logit has probability 0 everywhere.  With N = 0 (also T = 0, where
+ * unlike in other calls the outputs are written) loss, counts and
+ * probabilities are 0.  Sums over tokens are fp32 inside a block of rows and
+ * fp64 across blocks, in a fixed order.  Errors as moe_align_sort. */
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t k, int32_t E);
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                     int32_t T, int32_t E, int32_t k, float coef, float* loss,
+                     int32_t* expert_counts, float* expert_probs, int32_t* token_count, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* Gradient of that loss on the logits (the counts carry none):
+ *   grad_logits[t][i] = grad_loss coef E / N * p_ti (f_i - sum_e f_e p_te)
+ * for the tokens that count, 0 for the others.  expert_counts, token_count,
+ * token_mask and coef as in the forward call; grad_loss [1] fp32 on the
+ * device; grad_logits [T,E] fp32 out, every row written, not overlapping an
+ * input.  Errors as moe_topk_gating. */
+int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
+                              const int32_t* expert_counts, const int32_t* token_count, int32_t T,
+                              int32_t E, int32_t k, float coef, const float* grad_loss,
+                              float* grad_logits, void* stream);
+
+/* Gradient of moe_topk_gating's weights on the logits.  With w_j, g_j the
+ * weight and its gradient in slot j and S = sum_j w_j g_j:
+ *   renormalize = 1: grad_logits[id_j] = w_j (g_j - S), 0 for other experts;
+ *   renormalize = 0: grad_logits[e] = (e = id_j ? w_j g_j : 0) - p_e S, p the
+ *                    softmax over all experts.
+ *   topk_ids [T,k], topk_weights [T,k] as moe_topk_gating wrote them;
+ *   grad_weights [T,k] fp32; logits [T,E] (read with renormalize = 0 only,
+ *   may be NULL otherwise); token_mask as above (a token that does not count
+ *   gets a zero row); grad_logits [T,E] fp32 out, every row written, not
+ *   overlapping an input.
+ * A slot whose id lies outside [0, E) contributes nothing, slots that name
+ * one expert twice add up in slot order, and a NaN weight (the gating of a
+ * row without a finite logit) counts as 0.  Errors as moe_topk_gating. */
+int moe_topk_gating_backward(const float* logits, const int32_t* topk_ids,
+                             const float* topk_weights, const float* grad_weights,
+                             const uint8_t* token_mask, int32_t T, int32_t E, int32_t k,
+                             int32_t renormalize, float* grad_logits, void* stream);
+
+/* The sum of the two gradients above in one pass over the logits: what a
+ * training step of the router takes. */
+int moe_router_backward(const float* logits, const int32_t* topk_ids, const float* topk_weights,
+                        const float* grad_weights, const uint8_t* token_mask,
+                        const int32_t* expert_counts, const int32_t* token_count, int32_t T,
+                        int32_t E, int32_t k, int32_t renormalize, float coef,
+                        const float* grad_loss, float* grad_logits, void* stream);
 
 /* Inverse rotary position embedding fused with per-head FP8 quantisation:
  * the pages' second fused kernel, whose token count changes from call to
@@ -260,8 +350,8 @@ int moe_inv_rope_fp8_quant(const void* x, const int32_t* positions, const float*
  * SwiGLU, (FP8: h quantisation), down projection and aggregation, enqueued
  * back to back on `stream`, with no host synchronisation.  Every token row
  * of `out` is written exactly once.
- *   x [T,H], logits [T,E] fp32, w13 [E,2I,H], w13_scale [E] (FP8), w2
- *   [E,H,I], w2_scale [E] (FP8), out [T,H]; topk_ids / topk_weights are
+ *   x [T,H], logits [T,E] fp32, w13 [E,2I,H], w13_scale ([E] FP8, [E,2I]
+ *   INT8), w2 [E,H,I], w2_scale ([E] FP8, [E,H] INT8), out [T,H]; topk_ids / topk_weights are
  *   optional outputs (NULL = kept in the workspace, see
  *   moe_workspace_routing); ws of moe_workspace_bytes(s) bytes.
  * Errors: as the step entry points, all checked before anything is

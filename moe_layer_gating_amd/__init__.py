@@ -10,6 +10,8 @@ Tensor dtypes by mode (taken from the dtype of ``w13``):
   fp32 weights            -> fp32 mode: x, h, out fp32
   bf16 weights            -> bf16 mode: x, h, out bf16
   float8_e4m3fn or uint8  -> FP8 mode: e4m3 codes, fp32 scales [E]; x, h, out bf16
+  int8 weights            -> INT8 mode: int8 codes, fp32 scales per output
+                             channel (w13_scale [E,2I], w2_scale [E,H]); x, h, out bf16
 """
 from __future__ import annotations
 
@@ -18,7 +20,7 @@ import os
 
 import torch
 
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_INT8 = 0, 1, 2, 4
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe_gfx950.so")
 _lib = None
@@ -42,12 +44,15 @@ class moe_routing_offsets(ctypes.Structure):
 EXPORTS = ("moe_check_shape", "moe_workspace_bytes", "moe_status_string",
            "moe_align_sort_workspace_bytes", "moe_workspace_routing", "moe_topk_gating",
            "moe_align_sort", "moe_grouped_gemm_w13_swiglu", "moe_grouped_gemm_w2", "moe_combine",
-           "moe_act_quant_e4m3",
+           "moe_act_quant_e4m3", "moe_act_quant_i8", "moe_balance_loss_workspace_bytes",
+           "moe_balance_loss", "moe_balance_loss_backward", "moe_topk_gating_backward",
+           "moe_router_backward",
            "moe_fused_forward", "moe_fused_forward_events", "moe_router_logits",
            "moe_fused_forward_router", "moe_fused_forward_noalloc", "moe_inv_rope_fp8_quant")
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 # host-only calls whose return type is not a moe_status
-_NON_STATUS = ("moe_workspace_bytes", "moe_status_string", "moe_align_sort_workspace_bytes")
+_NON_STATUS = ("moe_workspace_bytes", "moe_status_string", "moe_align_sort_workspace_bytes",
+               "moe_balance_loss_workspace_bytes")
 NUM_STAGE_EVENTS = 9
 
 
@@ -76,6 +81,14 @@ def lib():
         L.moe_grouped_gemm_w2.argtypes = [S, P, P, P, P, P, P, P, sz, P]
         L.moe_combine.argtypes = [S, P, P, P, P, P]
         L.moe_act_quant_e4m3.argtypes = [P, ctypes.c_int64, P, P, P]
+        f32 = ctypes.c_float
+        L.moe_act_quant_i8.argtypes = [P, ctypes.c_int64, i32, P, P, P]
+        L.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, i32]
+        L.moe_balance_loss_workspace_bytes.restype = sz
+        L.moe_balance_loss.argtypes = [P, P, P, i32, i32, i32, f32, P, P, P, P, P, sz, P]
+        L.moe_balance_loss_backward.argtypes = [P, P, P, P, i32, i32, i32, f32, P, P, P]
+        L.moe_topk_gating_backward.argtypes = [P, P, P, P, P, i32, i32, i32, i32, P, P]
+        L.moe_router_backward.argtypes = [P, P, P, P, P, P, P, i32, i32, i32, i32, f32, P, P, P]
         L.moe_fused_forward.argtypes = [S, P, P, P, P, P, P, P, P, P, P, sz, P]
         L.moe_fused_forward_noalloc.argtypes = [S, P, P, P, P, P, P, P, P, P, P]
         L.moe_inv_rope_fp8_quant.argtypes = [P, P, P, i32, i32, i32, i32, i32, i32, P, P, P]
@@ -109,6 +122,59 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _need(ok, what):
+    if not ok:
+        raise MoeError(what)
+
+
+def _arg(t, name, dtype, shape, device):
+    """Address of a tensor argument, checked against its declared type, shape
+    and device (the kernels trust all three)."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise MoeError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s%s" % (
+            name, dtype, shape, device, t.dtype, tuple(t.shape), t.device,
+            "" if t.is_contiguous() else " (not contiguous)"))
+    return t.data_ptr()
+
+
+def _mask_arg(t, T, device):
+    if t is None:
+        return None
+    _need(t.dtype in (torch.uint8, torch.bool), "token_mask must be uint8 or bool, got %s" % t.dtype)
+    return _arg(t, "token_mask", t.dtype, (T,), device)
+
+
+def _gpu(t, name):
+    """The device of the tensor that leads a call."""
+    _need(t.is_cuda, "%s must live on the GPU" % name)
+    return t.device
+
+
+def _run(what, device, *args):
+    """Calls `what` on `device`'s current stream, with that device current."""
+    f = getattr(lib(), what)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+    _check(rc, what)
+
+
+def _check_i8(x, x_name, width, w, w_name, scale, ids=()):
+    """INT8 mode: operand types and the scale per output channel (a scale of
+    another mode's shape would be read out of range)."""
+    dev = _gpu(x, x_name)
+    _need(w.dim() == 3 and w.shape[2] == width, "%s must be [E, channels, %d]" % (w_name, width))
+    _arg(x, x_name, torch.bfloat16, (x.shape[0], width), dev)
+    _arg(w, w_name, torch.int8, tuple(w.shape), dev)
+    _need(scale is not None, "%s_scale is required in INT8 mode" % w_name)
+    _arg(scale, w_name + "_scale", torch.float32, tuple(w.shape[:2]), dev)
+    for name, t, n in ids:
+        if t is not None:
+            _arg(t, name, torch.int32, (n,), dev)
+
+
 def mode_of(w):
     if w.dtype == torch.float32:
         return MOE_F32
@@ -116,6 +182,8 @@ def mode_of(w):
         return MOE_BF16
     if w.dtype in (torch.float8_e4m3fn, torch.uint8):
         return MOE_FP8_E4M3
+    if w.dtype == torch.int8:
+        return MOE_INT8
     raise MoeError("unsupported weight dtype %s" % w.dtype)
 
 
@@ -211,10 +279,15 @@ def moe_grouped_gemm_w13_swiglu(x, w13, w13_scale, sorted_ids, expert_offsets, k
     E, I2, _ = w13.shape
     I = I2 // 2
     shape = make_shape(T, H, E, k, I, mode)
+    if mode == MOE_INT8:
+        _check_i8(x, "x", H, w13, "w13", w13_scale,
+                  (("sorted_ids", sorted_ids, T * k), ("expert_offsets", expert_offsets, E + 1)))
+        if h is not None:
+            _arg(h, "h", torch.bfloat16, (T * k, I), x.device)
     ws = workspace(shape, x.device) if ws is None else ws
     if h is None:
         h = torch.empty((T * k, I), dtype=act_dtype(mode), device=x.device)
-    if act_scales is None:
+    if act_scales is None and mode != MOE_INT8:  # INT8: a scale per row, kept in the workspace
         act_scales = torch.zeros(4, dtype=torch.float32, device=x.device)
     _check(lib().moe_grouped_gemm_w13_swiglu(ctypes.byref(shape), _ptr(x), _ptr(w13),
                                              _ptr(w13_scale), _ptr(sorted_ids),
@@ -230,6 +303,11 @@ def moe_grouped_gemm_w2(h, w2, w2_scale, expert_offsets, act_scales, k, ws=None,
     E, H, _ = w2.shape
     T = n_pairs // k
     shape = make_shape(T, H, E, k, I, mode)
+    if mode == MOE_INT8:
+        _need(n_pairs == T * k, "h must hold a multiple of k rows")
+        _check_i8(h, "h", I, w2, "w2", w2_scale, (("expert_offsets", expert_offsets, E + 1),))
+        if y is not None:
+            _arg(y, "y", torch.float32, (n_pairs, H), h.device)
     ws = workspace(shape, h.device) if ws is None else ws
     if y is None:
         y = torch.empty((n_pairs, H), dtype=torch.float32, device=h.device)
@@ -251,6 +329,122 @@ def moe_act_quant_e4m3(a, codes=None, scales=None):
     return codes, scales
 
 
+def moe_act_quant_i8(a, codes=None, scales=None):
+    """Per-row int8 codes of a bf16 tensor [..., n]: (codes int8 like a, scales
+    fp32 [...], the value of one code)."""
+    dev = _gpu(a, "a")
+    _need(a.dim() >= 1, "a must have at least one dimension")
+    lead, n = tuple(a.shape[:-1]), a.shape[-1]
+    if codes is None:
+        codes = torch.empty(a.shape, dtype=torch.int8, device=dev)
+    if scales is None:
+        scales = torch.empty(lead, dtype=torch.float32, device=dev)
+    _run("moe_act_quant_i8", dev, _arg(a, "a", torch.bfloat16, tuple(a.shape), dev),
+         scales.numel(), n, _arg(codes, "codes", torch.int8, tuple(a.shape), dev),
+         _arg(scales, "scales", torch.float32, lead, dev))
+    return codes, scales
+
+
+def moe_balance_loss_workspace_bytes(T, k, E):
+    return lib().moe_balance_loss_workspace_bytes(int(T), int(k), int(E))
+
+
+def balance_loss_workspace(T, k, E, device=None):
+    """Allocate a workspace of moe_balance_loss (torch uint8)."""
+    n = moe_balance_loss_workspace_bytes(T, k, E)
+    _need(n > 0, "invalid router shape T=%d k=%d E=%d" % (T, k, E))
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=None,
+                     expert_counts=None, expert_probs=None, token_count=None):
+    """Load-balance loss coef * E * sum_e f_e P_e of the router logits [T,E]
+    and the chosen experts topk_ids [T,k].  token_mask [T] (uint8 or bool,
+    0 = padding) leaves tokens out.  Returns (loss [1] fp32, expert_counts
+    [E] int32, expert_probs [E] fp32, token_count [1] int32)."""
+    dev = _gpu(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    if ws is None:
+        ws = balance_loss_workspace(T, k, E, dev)
+    if loss is None:
+        loss = torch.empty(1, dtype=torch.float32, device=dev)
+    if expert_counts is None:
+        expert_counts = torch.empty(E, dtype=torch.int32, device=dev)
+    if expert_probs is None:
+        expert_probs = torch.empty(E, dtype=torch.float32, device=dev)
+    if token_count is None:
+        token_count = torch.empty(1, dtype=torch.int32, device=dev)
+    _run("moe_balance_loss", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), _mask_arg(token_mask, T, dev), T, E,
+         k, coef, _arg(loss, "loss", torch.float32, (1,), dev),
+         _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
+         _arg(expert_probs, "expert_probs", torch.float32, (E,), dev),
+         _arg(token_count, "token_count", torch.int32, (1,), dev),
+         _arg(ws, "ws", torch.uint8, (ws.numel(),), dev), ws.numel())
+    return loss, expert_counts, expert_probs, token_count
+
+
+def _grad_buffer(grad_logits, logits, shape, dev):
+    if grad_logits is None:
+        return torch.empty(shape, dtype=torch.float32, device=dev)
+    _need(grad_logits.data_ptr() != logits.data_ptr() or grad_logits.numel() == 0,
+          "grad_logits must not overlap logits")
+    return grad_logits
+
+
+def moe_balance_loss_backward(logits, expert_counts, token_count, k, coef, grad_loss,
+                              token_mask=None, grad_logits=None):
+    """Gradient [T,E] of moe_balance_loss on the logits, from the counts it
+    returned; grad_loss [1] fp32."""
+    dev = _gpu(logits, "logits")
+    T, E = logits.shape
+    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
+    _run("moe_balance_loss_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
+         _mask_arg(token_mask, T, dev),
+         _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
+         _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k, coef,
+         _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),
+         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+    return grad_logits
+
+
+def moe_topk_gating_backward(logits, topk_ids, topk_weights, grad_weights, renormalize=True,
+                             token_mask=None, grad_logits=None):
+    """Gradient [T,E] on the logits of the gating weights moe_topk_gating
+    returned, from grad_weights [T,k]."""
+    dev = _gpu(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
+    _run("moe_topk_gating_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+         _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
+         _arg(grad_weights, "grad_weights", torch.float32, (T, k), dev),
+         _mask_arg(token_mask, T, dev), T, E, k, int(bool(renormalize)),
+         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+    return grad_logits
+
+
+def moe_router_backward(logits, topk_ids, topk_weights, grad_weights, expert_counts, token_count,
+                        coef, grad_loss, renormalize=True, token_mask=None, grad_logits=None):
+    """moe_topk_gating_backward plus moe_balance_loss_backward in one pass."""
+    dev = _gpu(logits, "logits")
+    T, E = logits.shape
+    k = topk_ids.shape[-1]
+    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
+    _run("moe_router_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
+         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev),
+         _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
+         _arg(grad_weights, "grad_weights", torch.float32, (T, k), dev),
+         _mask_arg(token_mask, T, dev),
+         _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
+         _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k,
+         int(bool(renormalize)), coef, _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),
+         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+    return grad_logits
+
+
 def moe_combine(y, inv_perm, topk_weights, mode, E=None, I=128, out=None):
     T, k = topk_weights.shape
     H = y.shape[1]
@@ -262,12 +456,31 @@ def moe_combine(y, inv_perm, topk_weights, mode, E=None, I=128, out=None):
     return out
 
 
+def _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits=None,
+                    topk_ids=None, topk_weights=None):
+    _check_i8(x, "x", H, w13, "w13", w13_scale)
+    _arg(w2, "w2", torch.int8, (E, H, I), x.device)
+    _need(w2_scale is not None, "w2_scale is required in INT8 mode")
+    _arg(w2_scale, "w2_scale", torch.float32, (E, H), x.device)
+    if out is not None:
+        _arg(out, "out", torch.bfloat16, (T, H), x.device)
+    if logits is not None:
+        _arg(logits, "logits", torch.float32, (T, E), x.device)
+    if topk_ids is not None:
+        _arg(topk_ids, "topk_ids", torch.int32, (T, k), x.device)
+    if topk_weights is not None:
+        _arg(topk_weights, "topk_weights", torch.float32, (T, k), x.device)
+
+
 def moe_fused_forward(x, logits, w13, w13_scale, w2, w2_scale, k, renormalize=True, out=None,
                       ws=None, topk_ids=None, topk_weights=None):
     mode = mode_of(w13)
     T, H = x.shape
     E, I2, _ = w13.shape
     I = I2 // 2
+    if mode == MOE_INT8:
+        _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
+                        topk_weights)
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:
@@ -286,6 +499,9 @@ def moe_fused_forward_noalloc(x, logits, w13, w13_scale, w2, w2_scale, k, out,
     mode = mode_of(w13)
     T, H = x.shape
     E, I2, _ = w13.shape
+    if mode == MOE_INT8:
+        _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I2 // 2, k, out, logits,
+                        topk_ids, topk_weights)
     shape = make_shape(T, H, E, k, I2 // 2, mode, renormalize)
     _check(lib().moe_fused_forward_noalloc(ctypes.byref(shape), _ptr(x), _ptr(logits), _ptr(w13),
                                            _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), _ptr(out),
@@ -337,6 +553,9 @@ def moe_fused_forward_router(x, wg, w13, w13_scale, w2, w2_scale, k, renormalize
     E, I2, _ = w13.shape
     I = I2 // 2
     assert tuple(wg.shape) == (E, H) and wg.dtype == act_dtype(mode)
+    if mode == MOE_INT8:
+        _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
+                        topk_weights)
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:
@@ -358,6 +577,9 @@ def moe_fused_forward_events(x, logits, w13, w13_scale, w2, w2_scale, k, events,
     T, H = x.shape
     E, I2, _ = w13.shape
     I = I2 // 2
+    if mode == MOE_INT8:
+        _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
+                        topk_weights)
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:

@@ -43,7 +43,7 @@ inline long max_tiles_for(long n_pairs, int E, int bm) {
 struct Layout {
   size_t ctrl, ids, wts, counts, offsets, sorted, inv, tiles, tiles_big, tiles_spread,
       chunk_counts, chunk_base,
-      rank, xpart, xq, hq, h, y, logits, rtiles, total;
+      rank, xpart, xq, hq, h, y, logits, rtiles, xs, hs, total;
   long max_tiles, max_tiles_big, max_rtiles;
 };
 
@@ -92,18 +92,20 @@ Layout layout_for(const moe_shape& s) {
   L.chunk_counts = take(n_chunks * s.E * 4);
   L.chunk_base = take(n_chunks * s.E * 4);
   L.rank = take(np * 4);
-  const bool fp8 = s.wdtype == MOE_FP8_E4M3;
+  const bool fp8 = s.wdtype == MOE_FP8_E4M3, i8 = s.wdtype == MOE_INT8;
   L.xpart = take(fp8 ? kXParts * 4 : 0);
-  L.xq = take(fp8 ? (size_t)s.T * s.H : 0);
-  L.hq = take(fp8 ? (size_t)np * s.I : 0);
+  L.xq = take(fp8 || i8 ? (size_t)s.T * s.H : 0);
+  L.hq = take(fp8 || i8 ? (size_t)np * s.I : 0);
   L.h = take((size_t)np * s.I * act_bytes(s.wdtype));
   L.y = take((size_t)np * s.H * 4);
   L.max_rtiles = ((long)s.T + kRouterBM - 1) / kRouterBM;
   L.logits = take((size_t)s.T * s.E * 4);
   L.rtiles = take((size_t)(L.max_rtiles + 1) * sizeof(Tile));
-  // last, so that adding it moved no other region (the GEMMs' speed
+  // after the rest, so that adding it moved no other region (the GEMMs' speed
   // depends on where x, h and y sit)
   L.tiles_spread = take((size_t)(L.max_tiles_big + 1) * sizeof(Tile));
+  L.xs = take(i8 ? (size_t)s.T * 4 : 0);  // INT8: a scale per row of x and of h
+  L.hs = take(i8 ? (size_t)np * 4 : 0);
   L.total = o;
   return L;
 }
@@ -132,6 +134,21 @@ AlignLayout align_layout_for(int T, int k, int E) {
   L.rank = take(np * 4);
   L.inv = take(np >= kChunkSortMin ? np * 4 : 0);
   L.total = o;
+  return L;
+}
+
+// Workspace of moe_balance_loss: the blocks' partial sums.
+struct LossLayout {
+  size_t probs, counts, tokens, total;
+};
+
+LossLayout loss_layout_for(int T, int E) {
+  LossLayout L;
+  const size_t nb = balance_loss_blocks(T);
+  L.probs = 0;
+  L.counts = align_up(nb * E * 4, 256);
+  L.tokens = L.counts + align_up(nb * E * 4, 256);
+  L.total = L.tokens + align_up(nb * 4, 256);
   return L;
 }
 
@@ -175,10 +192,14 @@ int moe_check_shape(const moe_shape* s) {
   if (!s) return MOE_ERR_INVALID_ARG;
   int rc = check_common(s->T, s->E, s->k);
   if (rc) return rc;
-  if (s->wdtype < MOE_F32 || s->wdtype > MOE_FP8_E4M3) return MOE_ERR_INVALID_ARG;
+  if (s->wdtype != MOE_F32 && s->wdtype != MOE_BF16 && s->wdtype != MOE_FP8_E4M3 &&
+      s->wdtype != MOE_INT8)
+    return MOE_ERR_INVALID_ARG;
   if (s->renormalize != 0 && s->renormalize != 1) return MOE_ERR_INVALID_ARG;
   if (s->H <= 0 || s->I <= 0) return MOE_ERR_INVALID_ARG;
   if (s->H % 128 || s->I % 128) return MOE_ERR_UNSUPPORTED;
+  // 128 * 127 * K stays below 2^31: an int8 dot product cannot overflow
+  if (s->wdtype == MOE_INT8 && (s->H > 131072 || s->I > 131072)) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -205,7 +226,8 @@ const char* moe_status_string(int status) {
   switch (status) {
     case MOE_OK: return "ok";
     case MOE_ERR_INVALID_ARG: return "invalid argument";
-    case MOE_ERR_UNSUPPORTED: return "unsupported shape (H and I must be multiples of 128)";
+    case MOE_ERR_UNSUPPORTED:
+      return "unsupported shape (H and I must be multiples of 128, at most 131072 for int8)";
     case MOE_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case MOE_ERR_HIP: return "HIP launch failure";
     case MOE_ERR_TOO_LARGE:
@@ -281,11 +303,11 @@ int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w
   int rc = moe_check_shape(s);
   if (rc) return rc;
   if (s->T == 0) return MOE_OK;
-  const bool fp8 = s->wdtype == MOE_FP8_E4M3;
+  const bool fp8 = s->wdtype == MOE_FP8_E4M3, i8 = s->wdtype == MOE_INT8;
   if (!x || !w13 || !sorted_ids || !expert_offsets || !h) return MOE_ERR_INVALID_ARG;
-  if (fp8 && (!w13_scale || !act_scales)) return MOE_ERR_INVALID_ARG;
+  if ((fp8 && (!w13_scale || !act_scales)) || (i8 && !w13_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(w13) || !aligned16(sorted_ids) || !aligned16(expert_offsets) ||
-      !aligned16(h) || (fp8 && (!aligned16(w13_scale) || !aligned16(act_scales))))
+      !aligned16(h) || (fp8 && !aligned16(act_scales)) || ((fp8 || i8) && !aligned16(w13_scale)))
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_ws(s, ws, ws_bytes))) return rc;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -301,6 +323,14 @@ int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w
   else
     MOE_TRY(launch_build_tiles(expert_offsets, s->E, kSkinnyBM, tiles, &ctrl->num_tiles, st));
   const void* b = x;
+  const uint32_t* act = &ctrl->amax_x_bits;
+  if (i8) {
+    int8_t* xq = at<int8_t>(ws, L.xq);
+    float* xs = at<float>(ws, L.xs);
+    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(x), s->T, s->H, xq, xs, st));
+    b = xq;
+    act = reinterpret_cast<const uint32_t*>(xs);
+  }
   if (fp8) {
     uint8_t* xq = at<uint8_t>(ws, L.xq);
     if ((rc = enqueue_quant(reinterpret_cast<const uint16_t*>(x), (long)s->T * s->H,
@@ -310,12 +340,12 @@ int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w
   }
   if (big)
     MOE_TRY(launch_w13_tiles(s->wdtype, tiles_bm(*s), b, w13, w13_scale, sorted_ids, tiles_big,
-                             &ctrl->num_tiles_big, (int)L.max_tiles_big, s->H, s->I, s->k,
-                             &ctrl->amax_x_bits, h, &ctrl->amax_h_bits, nullptr, nullptr, st));
+                             &ctrl->num_tiles_big, (int)L.max_tiles_big, s->H, s->I, s->k, act, h,
+                             &ctrl->amax_h_bits, nullptr, nullptr, st));
   else
     MOE_TRY(launch_w13_swiglu(s->wdtype, b, w13, w13_scale, sorted_ids, tiles, ctrl,
-                              (int)L.max_tiles, s->H, s->I, s->k, &ctrl->amax_x_bits, h,
-                              &ctrl->amax_h_bits, nullptr, nullptr, st));
+                              (int)L.max_tiles, s->H, s->I, s->k, act, h, &ctrl->amax_h_bits,
+                              nullptr, nullptr, st));
   if (fp8) MOE_TRY(launch_write_scales(ctrl, act_scales, st));
   return MOE_OK;
 }
@@ -326,11 +356,11 @@ int moe_grouped_gemm_w2(const moe_shape* s, const void* h, const void* w2, const
   int rc = moe_check_shape(s);
   if (rc) return rc;
   if (s->T == 0) return MOE_OK;
-  const bool fp8 = s->wdtype == MOE_FP8_E4M3;
+  const bool fp8 = s->wdtype == MOE_FP8_E4M3, i8 = s->wdtype == MOE_INT8;
   if (!h || !w2 || !expert_offsets || !y) return MOE_ERR_INVALID_ARG;
-  if (fp8 && (!w2_scale || !act_scales)) return MOE_ERR_INVALID_ARG;
+  if ((fp8 && (!w2_scale || !act_scales)) || (i8 && !w2_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(h) || !aligned16(w2) || !aligned16(expert_offsets) || !aligned16(y) ||
-      (fp8 && (!aligned16(w2_scale) || !aligned16(act_scales))))
+      (fp8 && !aligned16(act_scales)) || ((fp8 || i8) && !aligned16(w2_scale)))
     return MOE_ERR_INVALID_ARG;
   if ((rc = check_ws(s, ws, ws_bytes))) return rc;
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -353,6 +383,14 @@ int moe_grouped_gemm_w2(const moe_shape* s, const void* h, const void* w2, const
     MOE_TRY(launch_quant_e4m3(reinterpret_cast<const uint16_t*>(h), (long)s->T * s->k * s->I,
                               amax_h, hq, st));
     b = hq;
+  }
+  if (i8) {
+    int8_t* hq = at<int8_t>(ws, L.hq);
+    float* hs = at<float>(ws, L.hs);
+    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(h), (long)s->T * s->k, s->I, hq,
+                                 hs, st));
+    b = hq;
+    amax_h = reinterpret_cast<const uint32_t*>(hs);
   }
   if (big)
     MOE_TRY(launch_w2_tiles(s->wdtype, tiles_bm(*s), b, w2, w2_scale, tiles_big,
@@ -379,6 +417,16 @@ int moe_act_quant_e4m3(const void* a, int64_t n, uint8_t* codes, float* scales, 
   return MOE_OK;
 }
 
+int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, float* scales,
+                     void* stream) {
+  if (rows < 0 || rows >= (1L << 31) || n <= 0 || n % 8) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (!a || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(a), (long)rows, n,
+                                         codes, scales, reinterpret_cast<hipStream_t>(stream)));
+}
+
 int moe_inv_rope_fp8_quant(const void* x, const int32_t* positions, const float* cos_sin,
                            int32_t T, int32_t n_heads, int32_t head_dim, int32_t rot_dim,
                            int32_t max_pos, int32_t interleaved, uint8_t* codes, float* scales,
@@ -397,6 +445,88 @@ int moe_inv_rope_fp8_quant(const void* x, const int32_t* positions, const float*
   return hip_status(launch_inv_rope_fp8(reinterpret_cast<const uint16_t*>(x), positions, cos_sin,
                                         T, n_heads, head_dim, rot_dim, max_pos, interleaved != 0,
                                         codes, scales, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t k, int32_t E) {
+  if (check_common(T, E, k) != MOE_OK) return 0;
+  return loss_layout_for(T, E).total;
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                     int32_t T, int32_t E, int32_t k, float coef, float* loss,
+                     int32_t* expert_counts, float* expert_probs, int32_t* token_count, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int rc = check_common(T, E, k);
+  if (rc) return rc;
+  if (!loss || !expert_counts || !expert_probs || !token_count) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!logits || !topk_ids)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) || !aligned16(loss) ||
+      !aligned16(expert_counts) || !aligned16(expert_probs) || !aligned16(token_count))
+    return MOE_ERR_INVALID_ARG;
+  const LossLayout L = loss_layout_for(T, E);
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.total)
+    return MOE_ERR_WORKSPACE;
+  return hip_status(launch_balance_loss(
+      logits, topk_ids, T > 0 ? token_mask : nullptr, T, E, k, coef, loss, expert_counts,
+      expert_probs, token_count, at<float>(ws, L.probs), at<int32_t>(ws, L.counts),
+      at<int32_t>(ws, L.tokens), reinterpret_cast<hipStream_t>(stream)));
+}
+
+int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
+                              const int32_t* expert_counts, const int32_t* token_count, int32_t T,
+                              int32_t E, int32_t k, float coef, const float* grad_loss,
+                              float* grad_logits, void* stream) {
+  int rc = check_common(T, E, k);
+  if (rc) return rc;
+  if (T == 0) return MOE_OK;
+  if (!logits || !expert_counts || !token_count || !grad_loss || !grad_logits)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(token_mask) || !aligned16(expert_counts) ||
+      !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_router_grad(logits, nullptr, nullptr, nullptr, token_mask,
+                                       expert_counts, token_count, grad_loss, coef, 1, T, E, k,
+                                       grad_logits, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int moe_topk_gating_backward(const float* logits, const int32_t* topk_ids,
+                             const float* topk_weights, const float* grad_weights,
+                             const uint8_t* token_mask, int32_t T, int32_t E, int32_t k,
+                             int32_t renormalize, float* grad_logits, void* stream) {
+  int rc = check_common(T, E, k);
+  if (rc) return rc;
+  if (renormalize != 0 && renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!topk_ids || !topk_weights || !grad_weights || !grad_logits || (!renormalize && !logits))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
+      !aligned16(grad_weights) || !aligned16(token_mask) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_router_grad(logits, topk_ids, topk_weights, grad_weights, token_mask,
+                                       nullptr, nullptr, nullptr, 0.f, renormalize, T, E, k,
+                                       grad_logits, reinterpret_cast<hipStream_t>(stream)));
+}
+
+int moe_router_backward(const float* logits, const int32_t* topk_ids, const float* topk_weights,
+                        const float* grad_weights, const uint8_t* token_mask,
+                        const int32_t* expert_counts, const int32_t* token_count, int32_t T,
+                        int32_t E, int32_t k, int32_t renormalize, float coef,
+                        const float* grad_loss, float* grad_logits, void* stream) {
+  int rc = check_common(T, E, k);
+  if (rc) return rc;
+  if (renormalize != 0 && renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights || !grad_weights || !expert_counts || !token_count ||
+      !grad_loss || !grad_logits)
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
+      !aligned16(grad_weights) || !aligned16(token_mask) || !aligned16(expert_counts) ||
+      !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_router_grad(logits, topk_ids, topk_weights, grad_weights, token_mask,
+                                       expert_counts, token_count, grad_loss, coef, renormalize,
+                                       T, E, k, grad_logits,
+                                       reinterpret_cast<hipStream_t>(stream)));
 }
 
 int moe_combine(const moe_shape* s, const float* y, const int32_t* inv_perm,
@@ -420,6 +550,7 @@ int router_impl(const moe_shape* s, const void* x, const void* wg, float* logits
                 hipStream_t st) {
   const Layout L = layout_for(*s);
   Ctrl* ctrl = at<Ctrl>(ws, L.ctrl);
+  // INT8 layers, as FP8 ones, keep the router in bf16
   return hip_status(launch_router_logits(s->wdtype, x, wg, s->T, s->H, s->E, logits,
                                          at<Tile>(ws, L.rtiles), &ctrl->num_tiles_router,
                                          (int)L.max_rtiles, st));
@@ -456,13 +587,13 @@ int check_fused_args(const moe_shape* s, const void* x, const float* logits, con
                      const float* w13_scale, const void* w2, const float* w2_scale,
                      const void* out, const int32_t* topk_ids, const float* topk_weights,
                      void* ws, size_t ws_bytes) {
-  const bool fp8 = s->wdtype == MOE_FP8_E4M3;
+  const bool scaled = s->wdtype == MOE_FP8_E4M3 || s->wdtype == MOE_INT8;
   if (!x || !logits || !w13 || !w2 || !out) return MOE_ERR_INVALID_ARG;
-  if (fp8 && (!w13_scale || !w2_scale)) return MOE_ERR_INVALID_ARG;
+  if (scaled && (!w13_scale || !w2_scale)) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(logits) || !aligned16(w13) || !aligned16(w2) ||
       !aligned16(out) || (topk_ids && !aligned16(topk_ids)) ||
       (topk_weights && !aligned16(topk_weights)) ||
-      (fp8 && (!aligned16(w13_scale) || !aligned16(w2_scale))))
+      (scaled && (!aligned16(w13_scale) || !aligned16(w2_scale))))
     return MOE_ERR_INVALID_ARG;
   return check_ws(s, ws, ws_bytes);
 }
@@ -485,7 +616,7 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
   int rc = moe_check_shape(s);
   if (rc) return rc;
   if (s->T == 0) return MOE_OK;
-  const bool fp8 = s->wdtype == MOE_FP8_E4M3;
+  const bool fp8 = s->wdtype == MOE_FP8_E4M3, i8 = s->wdtype == MOE_INT8;
   if ((rc = check_fused_args(s, x, logits, w13, w13_scale, w2, w2_scale, out, topk_ids,
                              topk_weights, ws, ws_bytes)))
     return rc;
@@ -516,6 +647,10 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
   const Grouping grouping = grouping_for((long)T * k);
   uint8_t* xq = fp8 ? at<uint8_t>(ws, L.xq) : nullptr;
   const void* bx = fp8 ? static_cast<const void*>(xq) : x;
+  // what the GEMMs read of the activations' scales: FP8 amax words, INT8 a
+  // scale per row
+  const uint32_t* act_x = &ctrl->amax_x_bits;
+  const uint32_t* act_h = &ctrl->amax_h_bits;
 
   const int bm = big ? tiles_bm(*s) : kSkinnyBM;
   Tile* tl = big ? tiles_big : tiles;
@@ -533,6 +668,13 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
                       (long)T * k < 256L * E;
   Tile* tiles_w2 = spread ? at<Tile>(ws, L.tiles_spread) : tiles_big;
   MOE_TRY(mark(0));
+  if (i8) {
+    int8_t* codes = at<int8_t>(ws, L.xq);
+    float* xs = at<float>(ws, L.xs);
+    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(x), T, H, codes, xs, st));
+    bx = codes;
+    act_x = reinterpret_cast<const uint32_t*>(xs);
+  }
   if (grouping == Grouping::kOneBlock) {
     // the front kernel's second block quantises a small x; a large one goes
     // to the grid-wide passes after it (the kernel leaves amax(x) at 0)
@@ -573,12 +715,12 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
   }
   if (big)
     MOE_TRY(launch_w13_tiles(s->wdtype, tiles_bm(*s), bx, w13, w13_scale, sorted, tiles_big,
-                             &ctrl->num_tiles_big, (int)L.max_tiles_big, H, I, k,
-                             &ctrl->amax_x_bits, h, &ctrl->amax_h_bits, ev(4), ev(5), st));
+                             &ctrl->num_tiles_big, (int)L.max_tiles_big, H, I, k, act_x, h,
+                             &ctrl->amax_h_bits, ev(4), ev(5), st));
   else
     MOE_TRY(launch_w13_swiglu(s->wdtype, bx, w13, w13_scale, sorted, tiles, ctrl,
-                              (int)L.max_tiles, H, I, k, &ctrl->amax_x_bits, h,
-                              &ctrl->amax_h_bits, ev(4), ev(5), st));
+                              (int)L.max_tiles, H, I, k, act_x, h, &ctrl->amax_h_bits, ev(4),
+                              ev(5), st));
   const void* bh = h;
   if (fp8) {
     uint8_t* hq = at<uint8_t>(ws, L.hq);
@@ -586,17 +728,25 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
                               &ctrl->amax_h_bits, hq, st));
     bh = hq;
   }
-  // FP8 layers with many tokens per expert keep y in bf16 between the down
+  if (i8) {
+    int8_t* codes = at<int8_t>(ws, L.hq);
+    float* hs = at<float>(ws, L.hs);
+    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(h), (long)T * k, I, codes, hs,
+                                 st));
+    bh = codes;
+    act_h = reinterpret_cast<const uint32_t*>(hs);
+  }
+  // FP8 and INT8 layers with many tokens per expert keep y in bf16 between the down
   // projection and the aggregation (half the bytes of that round trip); the
   // step entry points return fp32 y
-  const bool y_bf16 = fp8 && big;
+  const bool y_bf16 = (fp8 || i8) && big;
   if (big)
     MOE_TRY(launch_w2_tiles(s->wdtype, tiles_bm(*s), bh, w2, w2_scale, tiles_w2,
-                            &ctrl->num_tiles_big, (int)L.max_tiles_big, H, I, &ctrl->amax_h_bits,
-                            y, y_bf16, ev(6), ev(7), st));
+                            &ctrl->num_tiles_big, (int)L.max_tiles_big, H, I, act_h, y, y_bf16,
+                            ev(6), ev(7), st));
   else
     MOE_TRY(launch_w2(s->wdtype, bh, w2, w2_scale, tiles, ctrl, (int)L.max_tiles, H, I,
-                      &ctrl->amax_h_bits, y, ev(6), ev(7), st));
+                      act_h, y, ev(6), ev(7), st));
   MOE_TRY(launch_combine(s->wdtype, y, y_bf16, inv, wts, T, H, k, out, st));
   MOE_TRY(mark(8));
   return MOE_OK;

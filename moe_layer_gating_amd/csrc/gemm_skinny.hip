@@ -40,6 +40,7 @@ struct Step;
 // bf16: one v_mfma_f32_16x16x32_bf16 per step; 8 bf16 (16 B) per lane.
 template <>
 struct Step<MOE_BF16> {
+  typedef f32x4 Acc;
   static constexpr int KS = 32;     // K elements per step
   static constexpr int LANE_K = 8;  // K elements per lane per step
   static constexpr int ES = 2;      // bytes per element
@@ -58,6 +59,7 @@ struct Step<MOE_BF16> {
 // sides, unit block scales) per step; 32 codes (32 B) per lane.
 template <>
 struct Step<MOE_FP8_E4M3> {
+  typedef f32x4 Acc;
   static constexpr int KS = 128;
   static constexpr int LANE_K = 32;
   static constexpr int ES = 1;
@@ -80,6 +82,7 @@ struct Step<MOE_FP8_E4M3> {
 // so a step sums the same 128 products.
 template <>
 struct Step<kFp8ViaBf16> {
+  typedef f32x4 Acc;
   static constexpr int KS = 128;
   static constexpr int LANE_K = 32;
   static constexpr int ES = 1;
@@ -102,6 +105,7 @@ struct Step<kFp8ViaBf16> {
 // the i-th MFMA of the step uses the lane's i-th float.
 template <>
 struct Step<MOE_F32> {
+  typedef f32x4 Acc;
   static constexpr int KS = 16;
   static constexpr int LANE_K = 4;
   static constexpr int ES = 4;
@@ -119,25 +123,46 @@ struct Step<MOE_F32> {
   }
 };
 
+// int8: two v_mfma_i32_16x16x64_i8 per step; 32 codes (32 B) per lane, the
+// u-th MFMA takes the lane's codes 16u .. 16u+15.  Exact 32-bit sums.
+template <>
+struct Step<MOE_INT8> {
+  typedef i32x4 Acc;
+  static constexpr int KS = 128;
+  static constexpr int LANE_K = 32;
+  static constexpr int ES = 1;
+  typedef i32x8 Frag;
+  static __device__ __forceinline__ Frag load(const char* p) {
+    return Step<MOE_FP8_E4M3>::load(p);
+  }
+  static __device__ __forceinline__ Frag zero() { return Step<MOE_FP8_E4M3>::zero(); }
+  static __device__ __forceinline__ i32x4 mma(Frag a, Frag b, i32x4 c) {
+    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{a[0], a[1], a[2], a[3]},
+                                              i32x4{b[0], b[1], b[2], b[3]}, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{a[4], a[5], a[6], a[7]},
+                                                 i32x4{b[4], b[5], b[6], b[7]}, c, 0, 0, 0);
+  }
+};
+
 // Steps of loads issued ahead of their MFMAs: 128 bytes per lane in every mode
 // (deeper unrolls and non-temporal weight loads both measured slower on the
 // decode shapes).
 template <int MODE>
 constexpr int unroll_for() {
-  return is_fp8(MODE) ? 4 : 8;
+  return is_fp8(MODE) || MODE == MOE_INT8 ? 4 : 8;
 }
 
 // Partial product of one wave: A row `arow` (this lane's weight row), B row
 // `brow` (this lane's token row, or nullptr for an empty column), over the
 // wave's steps [s0, s1).  U steps of loads are issued before their MFMAs.
 template <int MODE, int U>
-__device__ __forceinline__ f32x4 wave_dot(const char* __restrict__ arow,
+__device__ __forceinline__ typename Step<MODE>::Acc wave_dot(const char* __restrict__ arow,
                                           const char* __restrict__ brow,
                                           int s0, int s1, int g) {
   typedef Step<MODE> S;
   constexpr int STEP_BYTES = S::KS * S::ES;
   const int lane_off = g * S::LANE_K * S::ES;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  typename S::Acc acc = {0, 0, 0, 0};
   int s = s0;
   for (; s + U <= s1; s += U) {
     typename S::Frag a[U], b[U];
@@ -166,8 +191,8 @@ __device__ __forceinline__ float act_scale_from_bits(const uint32_t* bits) {
 
 // Sum the NW partial 16x16 products of the block's waves in a fixed order
 // ((w0 + w1) + w2) + ...; the result is valid in wave 0 only.
-template <int NW>
-__device__ __forceinline__ f32x4 block_reduce(f32x4 acc, float (*red)[64][4]) {
+template <int NW, typename Acc, typename V>
+__device__ __forceinline__ Acc block_reduce(Acc acc, V (*red)[64][4]) {
   const int lane = lane_id(), w = threadIdx.x / kWave;
   if (w > 0) {
 #pragma unroll
@@ -204,7 +229,7 @@ __global__ __launch_bounds__(NW * 64) void w13_swiglu_skinny(
     const Ctrl* __restrict__ ctrl, int H, int I, int k, const uint32_t* act_amax_bits,
     void* __restrict__ h, uint32_t* amax_h_bits) {
   typedef Step<MODE> S;
-  __shared__ float red[NW - 1][64][4];
+  __shared__ decltype(typename S::Acc{}[0] + 0) red[NW - 1][64][4];
   const int blocks_per_tile = I / 8;
   const int tile_idx = blockIdx.x / blocks_per_tile;
   const int rb = blockIdx.x - tile_idx * blocks_per_tile;
@@ -222,7 +247,7 @@ __global__ __launch_bounds__(NW * 64) void w13_swiglu_skinny(
   }
   const int n_steps = H / S::KS;
   const int s0 = (w * n_steps) / NW, s1 = ((w + 1) * n_steps) / NW;
-  f32x4 acc = wave_dot<MODE, U>(arow, brow, s0, s1, g);
+  typename S::Acc acc = wave_dot<MODE, U>(arow, brow, s0, s1, g);
   acc = block_reduce<NW>(acc, red);
   if (w != 0) return;
 
@@ -237,6 +262,12 @@ __global__ __launch_bounds__(NW * 64) void w13_swiglu_skinny(
       if (is_fp8(MODE)) {
         gv *= c;
         uv *= c;
+      }
+      if (MODE == MOE_INT8) {
+        const float sx = reinterpret_cast<const float*>(act_amax_bits)[sorted_ids[tl.p0 + r] / k];
+        const float* ws = w13_scale + (size_t)tl.e * 2 * I + n0 + 2 * g + q;
+        gv *= sx * ws[0];
+        uv *= sx * ws[I];
       }
       hv[q] = gv / (1.0f + expf(-gv)) * uv;
     }
@@ -269,7 +300,7 @@ __global__ __launch_bounds__(NW * 64) void w2_skinny(const char* __restrict__ b,
                                                      const uint32_t* act_amax_bits,
                                                      float* __restrict__ y) {
   typedef Step<MODE> S;
-  __shared__ float red[NW - 1][64][4];
+  __shared__ decltype(typename S::Acc{}[0] + 0) red[NW - 1][64][4];
   const int blocks_per_tile = H / 16;
   const int tile_idx = blockIdx.x / blocks_per_tile;
   const int rb = blockIdx.x - tile_idx * blocks_per_tile;
@@ -282,9 +313,14 @@ __global__ __launch_bounds__(NW * 64) void w2_skinny(const char* __restrict__ b,
   const char* brow = (r < tl.mt) ? b + (size_t)(tl.p0 + r) * I * S::ES : nullptr;
   const int n_steps = I / S::KS;
   const int s0 = (w * n_steps) / NW, s1 = ((w + 1) * n_steps) / NW;
-  f32x4 acc = wave_dot<MODE, U>(arow, brow, s0, s1, g);
-  acc = block_reduce<NW>(acc, red);
+  typename S::Acc sum = wave_dot<MODE, U>(arow, brow, s0, s1, g);
+  sum = block_reduce<NW>(sum, red);
   if (w != 0 || r >= tl.mt) return;
+  f32x4 acc = {(float)sum[0], (float)sum[1], (float)sum[2], (float)sum[3]};
+  if (MODE == MOE_INT8) {
+    const f32x4 ws = *reinterpret_cast<const f32x4*>(w2_scale + (size_t)tl.e * H + m0 + 4 * g);
+    acc *= ws * reinterpret_cast<const float*>(act_amax_bits)[tl.p0 + r];
+  }
   if (MODE == MOE_FP8_E4M3) acc *= act_scale_from_bits(act_amax_bits) * w2_scale[tl.e];
   *reinterpret_cast<f32x4*>(y + (size_t)(tl.p0 + r) * H + m0 + 4 * g) = acc;
 }
@@ -341,6 +377,9 @@ hipError_t launch_w13_swiglu(int mode, const void* b, const void* w13, const flo
   if (mode == MOE_F32)
     launch_w13_mode<MOE_F32>(max_tiles, bb, ww, w13_scale, sorted_ids, tiles, ctrl, H, I, k,
                              act_amax_bits, h, amax_h_bits, e0, e1, st);
+  else if (mode == MOE_INT8)
+    launch_w13_mode<MOE_INT8>(max_tiles, bb, ww, w13_scale, sorted_ids, tiles, ctrl, H, I, k,
+                              act_amax_bits, h, amax_h_bits, e0, e1, st);
   else if (mode == MOE_BF16)
     launch_w13_mode<MOE_BF16>(max_tiles, bb, ww, w13_scale, sorted_ids, tiles, ctrl, H, I, k,
                               act_amax_bits, h, amax_h_bits, e0, e1, st);
@@ -360,6 +399,9 @@ hipError_t launch_w2(int mode, const void* b, const void* w2, const float* w2_sc
   if (mode == MOE_F32)
     launch_w2_mode<MOE_F32>(max_tiles, bb, ww, w2_scale, tiles, ctrl, H, I, act_amax_bits, y, e0,
                             e1, st);
+  else if (mode == MOE_INT8)
+    launch_w2_mode<MOE_INT8>(max_tiles, bb, ww, w2_scale, tiles, ctrl, H, I, act_amax_bits, y, e0,
+                             e1, st);
   else if (mode == MOE_BF16)
     launch_w2_mode<MOE_BF16>(max_tiles, bb, ww, w2_scale, tiles, ctrl, H, I, act_amax_bits, y, e0,
                              e1, st);

@@ -198,12 +198,17 @@ hipError_t launch_router_logits(int mode, const void* x, const void* wg, int T, 
 hipError_t launch_amax_bf16(const uint16_t* src, long n, uint32_t* amax_bits, hipStream_t st);
 hipError_t launch_quant_e4m3(const uint16_t* src, long n, const uint32_t* amax_bits, uint8_t* dst,
                              hipStream_t st);
+// Per-row int8 codes and scales (amax / 127) of a bf16 matrix, n a multiple of 8.
+hipError_t launch_quant_i8_rows(const uint16_t* src, long rows, int n, int8_t* codes,
+                                float* scales, hipStream_t st);
 hipError_t launch_write_scales(const Ctrl* ctrl, float* act_scales, hipStream_t st);
 // scales[0] = amax / 448 (or 1) from the amax bits in scales[1].
 hipError_t launch_finish_scale(float* scales, hipStream_t st);
 // Grouped GEMMs.  `b` is the token-side operand: x (fp32/bf16) or the e4m3
 // codes of x (FP8) for w13; h (fp32/bf16) or the codes of h (FP8) for w2.
-// `act_amax_bits` (FP8 only) points at amax of that activation as fp32 bits.
+// `act_amax_bits` (FP8 only) points at amax of that activation as fp32 bits;
+// in INT8 mode it holds the activation's fp32 scale per row (per token for
+// w13, per sorted position for w2), and the weight scales are per channel.
 hipError_t launch_w13_swiglu(int mode, const void* b, const void* w13, const float* w13_scale,
                              const int32_t* sorted_ids, const Tile* tiles, const Ctrl* ctrl,
                              int max_tiles, int H, int I, int k, const uint32_t* act_amax_bits,
@@ -220,7 +225,7 @@ hipError_t launch_w13_tiles(int mode, int bm, const void* b, const void* w13,
                             const int32_t* num_tiles, int max_tiles, int H, int I, int k,
                             const uint32_t* act_amax_bits, void* h, uint32_t* amax_h_bits,
                             hipEvent_t e0, hipEvent_t e1, hipStream_t st);
-// y_bf16 (FP8 only): y is stored in bf16 instead of fp32.
+// y_bf16 (FP8 and INT8 only): y is stored in bf16 instead of fp32.
 hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, const float* w2_scale,
                            const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
                            int I, const uint32_t* act_amax_bits, void* y, bool y_bf16,
@@ -230,6 +235,21 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
 hipError_t launch_inv_rope_fp8(const uint16_t* x, const int32_t* positions, const float* cos_sin,
                                int T, int n_heads, int head_dim, int rot_dim, int max_pos,
                                bool interleaved, uint8_t* codes, float* scales, hipStream_t st);
+// Load-balance loss and router gradients (router_loss.hip).  The loss's
+// scratch holds balance_loss_blocks(T) * E floats and ints and
+// balance_loss_blocks(T) ints (unused when that is 1).  The gradient adds the
+// gating term when ids (with weights and grad_weights) are given and the
+// balance term when grad_loss (with counts and token_count) is.
+int balance_loss_blocks(int T);
+hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
+                               int E, int k, float coef, float* loss, int32_t* counts,
+                               float* probs, int32_t* token_count, float* part_p, int32_t* part_c,
+                               int32_t* part_n, hipStream_t st);
+hipError_t launch_router_grad(const float* logits, const int32_t* ids, const float* weights,
+                              const float* grad_weights, const uint8_t* mask,
+                              const int32_t* counts, const int32_t* token_count,
+                              const float* grad_loss, float coef, int renorm, int T, int E, int k,
+                              float* grad, hipStream_t st);
 // y [T*k,H] in sorted order, fp32 or (y_bf16, not in fp32 mode) bf16.
 hipError_t launch_combine(int mode, const void* y, bool y_bf16, const int32_t* inv_perm,
                           const float* w, int T, int H, int k, void* out, hipStream_t st);

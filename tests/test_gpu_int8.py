@@ -1,0 +1,296 @@
+"""The INT8 mode on the GPU: row codes, the grouped products with a scale per
+token and per output channel, and the whole layer on them, against the plain
+64-bit forms of plain64.  Codes and scales bit for bit; products within
+bounds that count their roundings (the integer sums are exact)."""
+import numpy as np
+import pytest
+import torch
+
+import moe_layer_gating_amd as moe
+import plain64 as P
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+
+def _bf16(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).bfloat16()
+
+
+def _np(t):
+    return t.detach().float().cpu().numpy().astype(np.float64)
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+# ------------------------------------------------------------------ row codes
+@pytest.mark.parametrize("rows,n", [(1, 8), (3, 128), (5, 2040), (4, 2048), (7, 2056), (3, 4104),
+                                    (2, 8192), (3, 16384), (2, 16392), (1, 131072), (1000, 256)])
+def test_row_codes(rows, n):
+    say("row codes", rows, n)
+    g = np.random.default_rng(rows * 31 + n)
+    a = _bf16(g.standard_normal((rows, n)) * np.exp(2 * g.standard_normal((rows, 1))))
+    a[0, ::5] = a[0].abs().max() / 2  # 63.5 codes: a tie
+    codes, scales = moe.moe_act_quant_i8(a.cuda())
+    wc, ws = P.quant_i8(_np(a))
+    assert np.array_equal(codes.cpu().numpy(), wc)
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
+    assert int(codes.max()) == 127 or int(codes.min()) == -127
+
+
+def test_row_codes_over_the_whole_range():
+    """Rows at every binade of bf16, subnormal ones too, zero rows, a row of
+    one value, every ratio of two bf16 significands."""
+    g = np.random.default_rng(1)
+    rows = []
+    for e in range(1, 255):
+        m = g.integers(0, 128, 256)
+        ex = np.maximum(e - g.integers(0, 9, 256), 0)
+        ex[0] = e
+        rows.append(((g.integers(0, 2, 256) << 15) | (ex << 7) | m).astype(np.uint16))
+    rows.append(np.zeros(256, np.uint16))
+    rows.append(np.full(256, 0x8000, np.uint16))
+    rows.append(np.arange(256, dtype=np.uint16) % 128)  # subnormal values only
+    for m in range(128):  # significand m against all others, one binade down
+        r = np.concatenate([np.arange(128), np.arange(128)]).astype(np.uint16)
+        r[:128] |= 126 << 7
+        r[128:] |= 125 << 7
+        r[255] = (127 << 7) | m
+        rows.append(r)
+    bits = np.stack(rows)
+    a = torch.from_numpy(bits.view(np.int16)).view(torch.bfloat16)
+    codes, scales = moe.moe_act_quant_i8(a.cuda())
+    wc, ws = P.quant_i8(_np(a))
+    assert np.array_equal(codes.cpu().numpy(), wc)
+    assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
+
+
+def test_row_codes_of_no_rows_and_other_shapes():
+    codes, scales = moe.moe_act_quant_i8(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"))
+    assert codes.shape == (0, 64) and scales.shape == (0,)
+    a = torch.randn(3, 4, 64, device="cuda").bfloat16()
+    codes, scales = moe.moe_act_quant_i8(a)
+    assert codes.shape == a.shape and scales.shape == (3, 4)
+    c2, s2 = moe.moe_act_quant_i8(a.view(12, 64))
+    assert torch.equal(codes.view(12, 64), c2) and torch.equal(scales.view(12), s2)
+
+
+# ------------------------------------------------------------------ products
+# name, T, H, E, k, I, skew: one token, one expert, k = E; few and many pairs
+# per expert (16-, 64- and 128-position tiles), tiles that end ragged, experts
+# without a pair, row counts that are and are not multiples of 256 channels,
+# reductions of one to many 128-code stages, the three groupings
+LAYERS = [
+    ("one_token", 1, 512, 16, 4, 256, 0.0),
+    ("one_expert", 5, 128, 1, 1, 128, 0.0),
+    ("k_is_E", 6, 256, 4, 4, 128, 0.0),
+    ("few_pairs", 16, 640, 16, 4, 384, 0.5),
+    ("few_pairs_many_experts", 40, 256, 64, 8, 256, 0.5),
+    ("tiles_64", 100, 384, 10, 3, 640, 0.3),
+    ("tiles_64_skewed", 211, 256, 8, 2, 256, 2.0),
+    ("tiles_128", 600, 512, 8, 2, 512, 0.3),
+    ("tiles_128_skewed", 1037, 384, 12, 3, 384, 2.0),
+    ("tiles_128_odd_rows", 400, 128, 3, 1, 128, 0.5),
+    ("chunked", 1100, 256, 16, 8, 128, 1.0),
+    ("large_experts", 1500, 512, 2, 1, 768, 0.2),
+]
+
+
+def _layer(T, H, E, k, I, skew, seed):
+    g = np.random.default_rng(seed)
+    x = _bf16(g.standard_normal((T, H)) * np.exp(g.standard_normal((T, 1))))
+    if T > 2:
+        x[1] = 0  # a padding row
+    logits = (g.standard_normal((T, E)) + skew * g.standard_normal(E)).astype(np.float32)
+    w13 = g.integers(-128, 128, (E, 2 * I, H)).astype(np.int8)
+    w2 = g.integers(-128, 128, (E, H, I)).astype(np.int8)
+    s13 = ((0.5 + g.random((E, 2 * I))) / (64 * H ** 0.5)).astype(np.float32)
+    s2 = ((0.5 + g.random((E, H))) / (64 * I ** 0.5)).astype(np.float32)
+    s13[0, :3] = 0
+    return x, logits, w13, s13, w2, s2
+
+
+def _grouping(logits, k):
+    E = logits.shape[1]
+    ids = np.argsort(-logits, 1, kind="stable")[:, :k].astype(np.int32)
+    flat = ids.reshape(-1)
+    order = np.argsort(flat, kind="stable").astype(np.int32)
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E))]).astype(np.int32)
+    inv = np.empty_like(order)
+    inv[order] = np.arange(order.size, dtype=np.int32)
+    return ids, order, offsets, inv
+
+
+def _within(got, want, bound, what):
+    got = np.asarray(got, np.float64)
+    assert np.all(np.isfinite(got)), what
+    worst = float(np.max(np.abs(got - want) / bound))
+    assert worst <= 1.0, "%s: %.3f of its bound" % (what, worst)
+
+
+@pytest.mark.parametrize("c", LAYERS, ids=[c[0] for c in LAYERS])
+def test_products_and_layer(c):
+    name, T, H, E, k, I, skew = c
+    say("int8", name)
+    x, logits, w13, s13, w2, s2 = _layer(T, H, E, k, I, skew, len(name) * 7 + T)
+    ids, order, offsets, inv = _grouping(logits, k)
+    dx, d13, d2 = x.cuda(), _dev(w13), _dev(w2)
+    ds13, ds2, doff, dord = _dev(s13), _dev(s2), _dev(offsets), _dev(order)
+    # rows behind the last pair stay as they are
+    hbuf = torch.full((T * k + 3, I), 5.0, dtype=torch.bfloat16, device="cuda")
+    h, _ = moe.moe_grouped_gemm_w13_swiglu(dx, d13, ds13, dord, doff, k, h=hbuf[:T * k])
+    want, bound = P.w13_i8(_np(x), w13, s13, order, offsets, k)
+    _within(_np(h), want, bound, "h")
+    assert torch.all(hbuf[T * k:] == 5.0)
+    ybuf = torch.full((T * k + 3, H), 5.0, device="cuda")
+    y = moe.moe_grouped_gemm_w2(h, d2, ds2, doff, None, k, y=ybuf[:T * k])
+    want, bound = P.w2_i8(_np(h), w2, s2, offsets)
+    _within(y.cpu().numpy(), want, bound, "y")
+    assert torch.all(ybuf[T * k:] == 5.0)
+    # the fused call is the steps in one: the same h, and y rounded to bf16
+    # between its product and the aggregation when the tiled kernels run
+    gids, gw = moe.moe_topk_gating(_dev(logits), k)
+    assert np.array_equal(gids.cpu().numpy(), ids)
+    y_in = y.bfloat16().float() if T * k >= 16 * E else y
+    steps = moe.moe_combine(y_in, _dev(inv), gw, moe.MOE_INT8, E=E, I=I)
+    out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    ids_out = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        moe.moe_fused_forward(dx, _dev(logits), d13, ds13, d2, ds2, k, out=out, topk_ids=ids_out)
+        assert torch.equal(out, steps), "fused and step results differ"
+        assert np.array_equal(ids_out.cpu().numpy(), ids)
+
+
+def test_longest_reduction_of_the_largest_codes():
+    """131072 products of 127 and -128: sums of -2 130 706 432, the largest
+    that the mode lets occur, in both tile classes."""
+    I, H = 131072, 128
+    w2 = np.full((1, H, I), -128, np.int8)
+    w2[0, 5] = 127
+    s2 = np.full((1, H), 0.5, np.float32)
+    for n in (3, 40):
+        h = torch.full((n, I), 3.0, dtype=torch.bfloat16)
+        h[1] = -0.75
+        offsets = np.array([0, n], np.int32)
+        y = moe.moe_grouped_gemm_w2(h.cuda(), _dev(w2), _dev(s2), _dev(offsets), None, 1)
+        want, bound = P.w2_i8(_np(h), w2, s2, offsets)
+        _within(y.cpu().numpy(), want, bound, "y")
+
+
+def test_weights_past_two_to_the_31_bytes():
+    """An expert whose codes start 2.1 GB into the tensor."""
+    E, N, K = 66, 8192, 4096
+    w2 = torch.zeros(E, N, K, dtype=torch.int8, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    last = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    w2[E - 1] = last
+    s2 = torch.rand(E, N, generator=g, device="cuda")
+    h = torch.randn(5, K, generator=g, device="cuda").bfloat16()
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[E] = 5
+    y = moe.moe_grouped_gemm_w2(h, w2, s2, offsets, None, 1)
+    want, bound = P.w2_i8(_np(h), last.cpu().numpy()[None], s2[E - 1:].cpu().numpy(),
+                          np.array([0, 5]))
+    _within(y.cpu().numpy(), want, bound, "y")
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_router_noalloc_events_and_graph(T):
+    """The layer's other entry points take int8 weights too: router in front,
+    static scratch, stage events, a captured graph replayed between eager
+    calls, a stream of its own."""
+    H, E, k, I = 256, 32, 4, 256
+    x, logits, w13, s13, w2, s2 = _layer(T, H, E, k, I, 0.5, T)
+    dx, d13, d2, ds13, ds2 = x.cuda(), _dev(w13), _dev(w2), _dev(s13), _dev(s2)
+    wg = _bf16(np.random.default_rng(2).standard_normal((E, H)) * 0.05).cuda()
+    lg = torch.empty(T, E, device="cuda")
+    out_r = moe.moe_fused_forward_router(dx, wg, d13, ds13, d2, ds2, k, logits=lg)
+    out = moe.moe_fused_forward(dx, lg, d13, ds13, d2, ds2, k)
+    assert torch.equal(out, out_r)
+    out_n = torch.empty_like(out)
+    moe.moe_fused_forward_noalloc(dx, lg, d13, ds13, d2, ds2, k, out_n)
+    assert torch.equal(out, out_n)
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(moe.NUM_STAGE_EVENTS)]
+    for e in ev:
+        e.record()
+    out_e = moe.moe_fused_forward_events(dx, lg, d13, ds13, d2, ds2, k, [e.cuda_event for e in ev])
+    torch.cuda.synchronize()
+    assert torch.equal(out, out_e) and ev[0].elapsed_time(ev[8]) >= 0
+    ws = moe.workspace(moe.make_shape(T, H, E, k, I, moe.MOE_INT8))
+    buf = torch.empty_like(out)
+
+    def step():
+        moe.moe_fused_forward(dx, lg, d13, ds13, d2, ds2, k, out=buf, ws=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for rep in range(4):
+        buf.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, out), "replay %d" % rep
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, out)
+
+
+def test_training_and_serving_steps_together():
+    """One batch as a router's training step takes it: the int8 layer, the
+    gradient of its gating weights (the derivative of <out, d> by w_tj is
+    <d_t, y_tj>), the balance loss and both gradients on the logits."""
+    T, H, E, k, I = 200, 256, 16, 4, 256
+    x, logits, w13, s13, w2, s2 = _layer(T, H, E, k, I, 0.5, 77)
+    mask = np.ones(T, np.uint8)
+    mask[150:] = 0
+    dl = _dev(logits)
+    ids, w = moe.moe_topk_gating(dl, k)
+    counts, offsets, order, inv = moe.moe_align_sort(ids, E)
+    h, _ = moe.moe_grouped_gemm_w13_swiglu(x.cuda(), _dev(w13), _dev(s13), order, offsets, k)
+    y = moe.moe_grouped_gemm_w2(h, _dev(w2), _dev(s2), offsets, None, k)
+    d = torch.randn(T, H, device="cuda")
+    gw = (y[inv.long()].view(T, k, H) * d[:, None]).sum(-1)
+    dm = _dev(mask)
+    loss, lcounts, probs, tokens = moe.moe_balance_loss(dl, ids, 0.01, token_mask=dm)
+    grad = moe.moe_router_backward(dl, ids, w, gw, lcounts, tokens, 0.01,
+                                   torch.ones(1, device="cuda"), token_mask=dm)
+    full = moe.moe_balance_loss(dl, ids, 0.01)[1]
+    assert torch.equal(full, counts)  # without a mask: the grouping's own counts
+    nids, nw, ngw = ids.cpu().numpy(), w.cpu().numpy(), gw.cpu().numpy()
+    a = P.gating_grad(logits, nids, nw, ngw, True, mask)
+    c32 = float(np.float32(0.01))
+    b = P.balance_grad(logits, lcounts.cpu().numpy(), 150, k, c32, 1.0, mask)
+    bound = P.gating_grad_bound(logits, nids, nw, ngw, True) + \
+        P.balance_grad_bound(logits, lcounts.cpu().numpy(), 150, k, c32, 1.0) + \
+        2 * P.U * (np.abs(a) + np.abs(b))
+    _within(grad.cpu().numpy(), a + b, bound, "router gradient")
+
+
+def test_refusals_on_the_gpu():
+    x = torch.randn(4, 256, device="cuda").bfloat16()
+    lg = torch.randn(4, 8, device="cuda")
+    w13 = torch.zeros(8, 512, 256, dtype=torch.int8, device="cuda")
+    w2 = torch.zeros(8, 256, 256, dtype=torch.int8, device="cuda")
+    s13, s2 = torch.ones(8, 512, device="cuda"), torch.ones(8, 256, device="cuda")
+    moe.moe_fused_forward(x, lg, w13, s13, w2, s2, 2)
+    for bad in ((x.float(), lg, w13, s13, w2, s2), (x, lg, w13, s13[:, 0].contiguous(), w2, s2),
+                (x, lg, w13, s13, w2, s2[:, 0].contiguous()), (x, lg, w13, None, w2, s2),
+                (x, lg, w13, s13, w2.view(torch.uint8), s2), (x, lg, w13, s13.double(), w2, s2),
+                (x, lg.double(), w13, s13, w2, s2), (x, lg, w13, s13, w2[:4], s2[:4])):
+        with pytest.raises(moe.MoeError):
+            moe.moe_fused_forward(*bad, 2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_act_quant_i8(x.float())
+    with pytest.raises(moe.MoeError):
+        moe.moe_act_quant_i8(torch.zeros(2, 12, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(moe.MoeError):
+        moe.moe_grouped_gemm_w2(x, w2, s2, torch.zeros(8, dtype=torch.int32, device="cuda"), None, 2)
