@@ -127,38 +127,42 @@ def _need(ok, what):
         raise MoeError(what)
 
 
-def _arg(t, name, dtype, shape, device):
+def _arg(t, name, dtype, shape, dev):
     """Address of a tensor argument, checked against its declared type, shape
-    and device (the kernels trust all three)."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
-        raise MoeError("%s must be a contiguous %s tensor of shape %s on %s, got %s %s on %s%s" % (
-            name, dtype, shape, device, t.dtype, tuple(t.shape), t.device,
+    and device index (the kernels trust all three)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise MoeError("%s must be a contiguous %s tensor of shape %s on GPU %d, got %s %s on %s%s" % (
+            name, dtype, tuple(shape), dev, t.dtype, tuple(t.shape), t.device,
             "" if t.is_contiguous() else " (not contiguous)"))
     return t.data_ptr()
 
 
-def _mask_arg(t, T, device):
+def _mask_arg(t, T, dev):
     if t is None:
         return None
-    _need(t.dtype in (torch.uint8, torch.bool), "token_mask must be uint8 or bool, got %s" % t.dtype)
-    return _arg(t, "token_mask", t.dtype, (T,), device)
+    _need(t.dtype is torch.uint8 or t.dtype is torch.bool,
+          "token_mask must be uint8 or bool, got %s" % t.dtype)
+    return _arg(t, "token_mask", t.dtype, (T,), dev)
 
 
 def _gpu(t, name):
-    """The device of the tensor that leads a call."""
-    _need(t.is_cuda, "%s must live on the GPU" % name)
-    return t.device
+    """Device index of the tensor that leads a call."""
+    dev = t.get_device()
+    if dev < 0:
+        raise MoeError("%s must live on the GPU" % name)
+    return dev
 
 
-def _run(what, device, *args):
-    """Calls `what` on `device`'s current stream, with that device current."""
-    f = getattr(lib(), what)
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
+def _run(what, dev, *args):
+    """Calls `what` on GPU `dev`'s current stream, with that GPU current."""
+    f = getattr(_lib or lib(), what)
+    if dev == torch.cuda.current_device():
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = f(*args, torch.cuda.current_stream(device).cuda_stream)
-    _check(rc, what)
+        with torch.cuda.device(dev):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if rc != 0:
+        _check(rc, what)
 
 
 def _check_i8(x, x_name, width, w, w_name, scale, ids=()):
@@ -167,9 +171,9 @@ def _check_i8(x, x_name, width, w, w_name, scale, ids=()):
     dev = _gpu(x, x_name)
     _need(w.dim() == 3 and w.shape[2] == width, "%s must be [E, channels, %d]" % (w_name, width))
     _arg(x, x_name, torch.bfloat16, (x.shape[0], width), dev)
-    _arg(w, w_name, torch.int8, tuple(w.shape), dev)
+    _arg(w, w_name, torch.int8, w.shape, dev)
     _need(scale is not None, "%s_scale is required in INT8 mode" % w_name)
-    _arg(scale, w_name + "_scale", torch.float32, tuple(w.shape[:2]), dev)
+    _arg(scale, w_name + "_scale", torch.float32, w.shape[:2], dev)
     for name, t, n in ids:
         if t is not None:
             _arg(t, name, torch.int32, (n,), dev)
@@ -283,7 +287,7 @@ def moe_grouped_gemm_w13_swiglu(x, w13, w13_scale, sorted_ids, expert_offsets, k
         _check_i8(x, "x", H, w13, "w13", w13_scale,
                   (("sorted_ids", sorted_ids, T * k), ("expert_offsets", expert_offsets, E + 1)))
         if h is not None:
-            _arg(h, "h", torch.bfloat16, (T * k, I), x.device)
+            _arg(h, "h", torch.bfloat16, (T * k, I), x.get_device())
     ws = workspace(shape, x.device) if ws is None else ws
     if h is None:
         h = torch.empty((T * k, I), dtype=act_dtype(mode), device=x.device)
@@ -307,7 +311,7 @@ def moe_grouped_gemm_w2(h, w2, w2_scale, expert_offsets, act_scales, k, ws=None,
         _need(n_pairs == T * k, "h must hold a multiple of k rows")
         _check_i8(h, "h", I, w2, "w2", w2_scale, (("expert_offsets", expert_offsets, E + 1),))
         if y is not None:
-            _arg(y, "y", torch.float32, (n_pairs, H), h.device)
+            _arg(y, "y", torch.float32, (n_pairs, H), h.get_device())
     ws = workspace(shape, h.device) if ws is None else ws
     if y is None:
         y = torch.empty((n_pairs, H), dtype=torch.float32, device=h.device)
@@ -334,13 +338,13 @@ def moe_act_quant_i8(a, codes=None, scales=None):
     fp32 [...], the value of one code)."""
     dev = _gpu(a, "a")
     _need(a.dim() >= 1, "a must have at least one dimension")
-    lead, n = tuple(a.shape[:-1]), a.shape[-1]
+    lead, n = a.shape[:-1], a.shape[-1]
     if codes is None:
         codes = torch.empty(a.shape, dtype=torch.int8, device=dev)
     if scales is None:
         scales = torch.empty(lead, dtype=torch.float32, device=dev)
-    _run("moe_act_quant_i8", dev, _arg(a, "a", torch.bfloat16, tuple(a.shape), dev),
-         scales.numel(), n, _arg(codes, "codes", torch.int8, tuple(a.shape), dev),
+    _run("moe_act_quant_i8", dev, _arg(a, "a", torch.bfloat16, a.shape, dev),
+         scales.numel(), n, _arg(codes, "codes", torch.int8, a.shape, dev),
          _arg(scales, "scales", torch.float32, lead, dev))
     return codes, scales
 
@@ -363,8 +367,9 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=
     0 = padding) leaves tokens out.  Returns (loss [1] fp32, expert_counts
     [E] int32, expert_probs [E] fp32, token_count [1] int32)."""
     dev = _gpu(logits, "logits")
-    T, E = logits.shape
+    T, E = shape = logits.shape
     k = topk_ids.shape[-1]
+    pairs = (T, k)
     if ws is None:
         ws = balance_loss_workspace(T, k, E, dev)
     if loss is None:
@@ -375,13 +380,13 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=
         expert_probs = torch.empty(E, dtype=torch.float32, device=dev)
     if token_count is None:
         token_count = torch.empty(1, dtype=torch.int32, device=dev)
-    _run("moe_balance_loss", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
-         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev), _mask_arg(token_mask, T, dev), T, E,
+    _run("moe_balance_loss", dev, _arg(logits, "logits", torch.float32, shape, dev),
+         _arg(topk_ids, "topk_ids", torch.int32, pairs, dev), _mask_arg(token_mask, T, dev), T, E,
          k, coef, _arg(loss, "loss", torch.float32, (1,), dev),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(expert_probs, "expert_probs", torch.float32, (E,), dev),
          _arg(token_count, "token_count", torch.int32, (1,), dev),
-         _arg(ws, "ws", torch.uint8, (ws.numel(),), dev), ws.numel())
+         _arg(ws, "ws", torch.uint8, ws.shape, dev), ws.numel())
     return loss, expert_counts, expert_probs, token_count
 
 
@@ -398,14 +403,14 @@ def moe_balance_loss_backward(logits, expert_counts, token_count, k, coef, grad_
     """Gradient [T,E] of moe_balance_loss on the logits, from the counts it
     returned; grad_loss [1] fp32."""
     dev = _gpu(logits, "logits")
-    T, E = logits.shape
-    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
-    _run("moe_balance_loss_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
+    T, E = shape = logits.shape
+    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    _run("moe_balance_loss_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
          _mask_arg(token_mask, T, dev),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k, coef,
          _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),
-         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+         _arg(grad_logits, "grad_logits", torch.float32, shape, dev))
     return grad_logits
 
 
@@ -414,15 +419,16 @@ def moe_topk_gating_backward(logits, topk_ids, topk_weights, grad_weights, renor
     """Gradient [T,E] on the logits of the gating weights moe_topk_gating
     returned, from grad_weights [T,k]."""
     dev = _gpu(logits, "logits")
-    T, E = logits.shape
+    T, E = shape = logits.shape
     k = topk_ids.shape[-1]
-    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
-    _run("moe_topk_gating_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
-         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-         _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
-         _arg(grad_weights, "grad_weights", torch.float32, (T, k), dev),
+    pairs = (T, k)
+    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    _run("moe_topk_gating_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
+         _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
+         _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),
+         _arg(grad_weights, "grad_weights", torch.float32, pairs, dev),
          _mask_arg(token_mask, T, dev), T, E, k, int(bool(renormalize)),
-         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+         _arg(grad_logits, "grad_logits", torch.float32, shape, dev))
     return grad_logits
 
 
@@ -430,18 +436,19 @@ def moe_router_backward(logits, topk_ids, topk_weights, grad_weights, expert_cou
                         coef, grad_loss, renormalize=True, token_mask=None, grad_logits=None):
     """moe_topk_gating_backward plus moe_balance_loss_backward in one pass."""
     dev = _gpu(logits, "logits")
-    T, E = logits.shape
+    T, E = shape = logits.shape
     k = topk_ids.shape[-1]
-    grad_logits = _grad_buffer(grad_logits, logits, (T, E), dev)
-    _run("moe_router_backward", dev, _arg(logits, "logits", torch.float32, (T, E), dev),
-         _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev),
-         _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev),
-         _arg(grad_weights, "grad_weights", torch.float32, (T, k), dev),
+    pairs = (T, k)
+    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    _run("moe_router_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
+         _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
+         _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),
+         _arg(grad_weights, "grad_weights", torch.float32, pairs, dev),
          _mask_arg(token_mask, T, dev),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k,
          int(bool(renormalize)), coef, _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),
-         _arg(grad_logits, "grad_logits", torch.float32, (T, E), dev))
+         _arg(grad_logits, "grad_logits", torch.float32, shape, dev))
     return grad_logits
 
 
@@ -459,17 +466,18 @@ def moe_combine(y, inv_perm, topk_weights, mode, E=None, I=128, out=None):
 def _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits=None,
                     topk_ids=None, topk_weights=None):
     _check_i8(x, "x", H, w13, "w13", w13_scale)
-    _arg(w2, "w2", torch.int8, (E, H, I), x.device)
+    dev = x.get_device()
+    _arg(w2, "w2", torch.int8, (E, H, I), dev)
     _need(w2_scale is not None, "w2_scale is required in INT8 mode")
-    _arg(w2_scale, "w2_scale", torch.float32, (E, H), x.device)
+    _arg(w2_scale, "w2_scale", torch.float32, (E, H), dev)
     if out is not None:
-        _arg(out, "out", torch.bfloat16, (T, H), x.device)
+        _arg(out, "out", torch.bfloat16, (T, H), dev)
     if logits is not None:
-        _arg(logits, "logits", torch.float32, (T, E), x.device)
+        _arg(logits, "logits", torch.float32, (T, E), dev)
     if topk_ids is not None:
-        _arg(topk_ids, "topk_ids", torch.int32, (T, k), x.device)
+        _arg(topk_ids, "topk_ids", torch.int32, (T, k), dev)
     if topk_weights is not None:
-        _arg(topk_weights, "topk_weights", torch.float32, (T, k), x.device)
+        _arg(topk_weights, "topk_weights", torch.float32, (T, k), dev)
 
 
 def moe_fused_forward(x, logits, w13, w13_scale, w2, w2_scale, k, renormalize=True, out=None,

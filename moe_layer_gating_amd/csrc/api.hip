@@ -146,8 +146,9 @@ LossLayout loss_layout_for(int T, int E) {
   LossLayout L;
   const size_t nb = balance_loss_blocks(T);
   L.probs = 0;
-  L.counts = align_up(nb * E * 4, 256);
-  L.tokens = L.counts + align_up(nb * E * 4, 256);
+  const size_t sums = align_up(nb * align_up((size_t)E, 4) * 4, 256);
+  L.counts = sums;
+  L.tokens = 2 * sums;
   L.total = L.tokens + align_up(nb * 4, 256);
   return L;
 }

@@ -236,8 +236,8 @@ hipError_t launch_inv_rope_fp8(const uint16_t* x, const int32_t* positions, cons
                                int T, int n_heads, int head_dim, int rot_dim, int max_pos,
                                bool interleaved, uint8_t* codes, float* scales, hipStream_t st);
 // Load-balance loss and router gradients (router_loss.hip).  The loss's
-// scratch holds balance_loss_blocks(T) * E floats and ints and
-// balance_loss_blocks(T) ints (unused when that is 1).  The gradient adds the
+// scratch holds balance_loss_blocks(T) rows of E (rounded up to 4) floats and
+// of as many ints, and balance_loss_blocks(T) ints (unused when that is 1).  The gradient adds the
 // gating term when ids (with weights and grad_weights) are given and the
 // balance term when grad_loss (with counts and token_count) is.
 int balance_loss_blocks(int T);

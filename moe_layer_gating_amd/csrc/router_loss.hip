@@ -25,7 +25,9 @@
 namespace moe {
 
 constexpr int kRowLanes = 16;  // lanes per logits row (k <= 16: a lane per slot too)
-constexpr int kLossThreads = 512;
+// threads of a loss block: 64 rows at a time (32 for the widest rows, whose
+// per-wave sums would not fit in LDS)
+__host__ __device__ constexpr int loss_threads(int nc) { return nc > 8 ? 512 : 1024; }
 constexpr int kGradThreads = 256;
 
 // Sum / maximum over the 16 lanes of a DPP row; every lane gets it.
@@ -47,6 +49,13 @@ __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, dpp<0x141>(v));
   v = fmaxf(v, dpp<0x140>(v));
   return v;
+}
+
+// Orders a wave's LDS accesses: its earlier writes are seen by its lanes.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Value q = 4c + i of lane l is expert (c * 16 + l) * 4 + i when E is a
@@ -77,6 +86,19 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
   }
 }
 
+// e^x for x <= 0 within about 2 steps: 2^y with y = fl(x log2 e), corrected by
+// the part of x log2 e that y lost (7 instructions; the library's expf takes
+// about twice as many, most of them for overflow and subnormal results, which
+// a softmax does not need: results below 2^-126 become 0).
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float kLog2e = 1.44269502f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147182f;
+  x = fmaxf(x, -128.0f);  // keeps the correction finite for -inf
+  const float y = x * kLog2e;
+  const float lost = fmaf(x, kLog2eLo, fmaf(x, kLog2e, -y));
+  const float e = __builtin_amdgcn_exp2f(y);
+  return fmaf(e, lost * kLn2, e);
+}
+
 // Softmax of a row in place; NaN reads as -inf (as the gating reads it), and
 // a row without a finite logit becomes all zero.
 template <int N>
@@ -92,7 +114,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[N]) {
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < N; q++) {
-    v[q] = expf(v[q] - m);
+    v[q] = exp_neg(v[q] - m);
     s += v[q];
   }
   s = row_sum(s);
@@ -101,68 +123,90 @@ __device__ __forceinline__ void softmax_row(float (&v)[N]) {
   for (int q = 0; q < N; q++) v[q] *= inv;
 }
 
-// Turns the sums over all tokens into the outputs; called by every thread of
-// one block.  sum_p / sum_c: E sums in LDS.  red: one double per wave.
-__device__ void finish_loss(const double* sum_p, const int* sum_c, int n, int E, int k, float coef,
-                            float* loss, int32_t* counts, float* probs, int32_t* token_count,
-                            double* red) {
-  const double inv_n = n > 0 ? 1.0 / n : 0.0;
+__device__ __forceinline__ bool row_live(const uint8_t* mask, long r, long end) {
+  return r < end && (!mask || mask[r]);
+}
+
+// Turns expert e's sums over all tokens (thread e < E holds them) into the
+// outputs; called by every thread of one block.  red: one double per wave.
+__device__ __forceinline__ void finish_loss(double sum_p, int sum_c, int n, int E, int k,
+                                            float coef, float* loss, int32_t* counts,
+                                            float* probs, int32_t* token_count, double* red) {
+  const int e = threadIdx.x;
+  const double inv_n = n > 0 ? 1.0 / n : 0.0, p = sum_p * inv_n;
   double part = 0.0;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    const double p = sum_p[e] * inv_n;
-    counts[e] = sum_c[e];
+  if (e < E) {
+    counts[e] = sum_c;
     probs[e] = (float)p;
-    part += sum_c[e] * p;
+    part = sum_c * p;
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
-  if (lane_id() == 0) red[threadIdx.x / kWave] = part;
+  if (lane_id() == 0) red[e / kWave] = part;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (e == 0) {
     double s = 0.0;
-    for (int w = 0; w < (int)blockDim.x / kWave; w++) s += red[w];
+    for (int w = 0; w < (E + kWave - 1) / kWave; w++) s += red[w];
     *loss = (float)((double)coef * E * s * inv_n / k);
     *token_count = n;
   }
 }
 
 // Block b sums the probabilities and counts of rows [b rows, (b + 1) rows)
-// into part_p[b], part_c[b], part_n[b]; a single block writes the outputs.
+// into row b of part_p and part_c (e4 values each) and part_n[b]; a single
+// block writes the outputs itself.
 template <int NC, bool VEC>
-__global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(
+__global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ mask, int T, int E, int k, int rows, float coef,
     float* __restrict__ part_p, int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ probs,
     int32_t* __restrict__ token_count) {
-  constexpr int N = 4 * NC, NW = kLossThreads / kWave, E_MAX = N * kRowLanes;
+  constexpr int N = 4 * NC, THREADS = loss_threads(NC), NW = THREADS / kWave;
+  constexpr int E_MAX = N * kRowLanes, STEP = THREADS / kRowLanes;
   __shared__ float wsum[NW][E_MAX];
   __shared__ int hist[E_MAX];
-  __shared__ double total[E_MAX];
   __shared__ double red[NW];
   __shared__ int n_live;
   const int t = threadIdx.x, l = t % kRowLanes, w = t / kWave;
-  const int lo = blockIdx.x * rows, hi = min(T, lo + rows);
-  for (int e = t; e < E; e += kLossThreads) hist[e] = 0;
+  const long lo = (long)blockIdx.x * rows, hi = min((long)T, lo + rows);
+  for (int e = t; e < E; e += THREADS) hist[e] = 0;
   if (t == 0) n_live = 0;
-  __syncthreads();
 
-  float acc[N];
+  // rows r, r + STEP, ...: the next row is on its way while one is summed
+  // (two buffers in turn: a copy would wait for the load), and the mask byte
+  // of the one after it
+  float acc[N], v[N], w2[N];
 #pragma unroll
   for (int q = 0; q < N; q++) acc[q] = 0.f;
+  const long f0 = lo * k + t;
+  const int id0 = f0 < hi * k && (!mask || mask[f0 / k]) ? ids[f0] : -1;
+  long r = lo + t / kRowLanes;
   int live = 0;
-  for (int r = lo + t / kRowLanes; r < hi; r += kLossThreads / kRowLanes) {
-    if (mask && !mask[r]) continue;  // the same for the row's 16 lanes
-    float v[N];
-    load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
-    softmax_row(v);
-#pragma unroll
-    for (int q = 0; q < N; q++) acc[q] += v[q];
-    live++;
-  }
-  for (size_t f = (size_t)lo * k + t; f < (size_t)hi * k; f += kLossThreads) {
+  bool on = row_live(mask, r, hi), on1 = row_live(mask, r + STEP, hi);
+  if (on) load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
+  __syncthreads();
+  if ((unsigned)id0 < (unsigned)E) atomicAdd(&hist[id0], 1);
+  for (long f = f0 + THREADS; f < hi * k; f += THREADS) {
     const int e = ids[f];
     if ((unsigned)e < (unsigned)E && (!mask || mask[f / k])) atomicAdd(&hist[e], 1);
+  }
+  auto round = [&](float(&cur)[N], float(&next)[N]) {
+    const bool on2 = row_live(mask, r + 2 * STEP, hi);
+    if (on1) load_row<NC, VEC>(logits + (size_t)(r + STEP) * E, E, l, next, -INFINITY);
+    if (on) {
+      softmax_row(cur);
+#pragma unroll
+      for (int q = 0; q < N; q++) acc[q] += cur[q];
+      live++;
+    }
+    on = on1;
+    on1 = on2;
+    r += STEP;
+  };
+  while (r < hi) {
+    round(v, w2);
+    round(w2, v);  // past the last row: nothing is on
   }
   if (l == 0 && live) atomicAdd(&n_live, live);
   // the wave's four rows, then the waves in order
@@ -178,16 +222,17 @@ __global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(
       for (int i = 0; i < 4; i++) wsum[w][expert_of<VEC>(c, i, l)] = acc[4 * c + i];
   }
   __syncthreads();
+  const int e4 = (E + 3) & ~3;
   const bool single = gridDim.x == 1;
-  for (int e = t; e < E; e += kLossThreads) {
+  for (int e = t; e < (single ? E : e4); e += THREADS) {
     float s = 0.f;
 #pragma unroll
     for (int q = 0; q < NW; q++) s += wsum[q][e];
     if (single) {
-      total[e] = s;
+      wsum[0][e] = s;  // read by this thread alone until the barrier below
     } else {
-      part_p[(size_t)blockIdx.x * E + e] = s;
-      part_c[(size_t)blockIdx.x * E + e] = hist[e];
+      part_p[(size_t)blockIdx.x * e4 + e] = s;
+      part_c[(size_t)blockIdx.x * e4 + e] = e < E ? hist[e] : 0;
     }
   }
   if (!single) {
@@ -195,46 +240,84 @@ __global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(
     return;
   }
   __syncthreads();
-  finish_loss(total, hist, n_live, E, k, coef, loss, counts, probs, token_count, red);
+  if constexpr (E_MAX > THREADS) {  // more experts than threads: two each
+    const double inv_n = n_live > 0 ? 1.0 / n_live : 0.0;
+    double part = 0.0;
+    for (int e = t; e < E; e += THREADS) {
+      const double p = wsum[0][e] * inv_n;
+      counts[e] = hist[e];
+      probs[e] = (float)p;
+      part += hist[e] * p;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
+    if (lane_id() == 0) red[w] = part;
+    __syncthreads();
+    if (t == 0) {
+      double s = 0.0;
+      for (int q = 0; q < NW; q++) s += red[q];
+      *loss = (float)((double)coef * E * s * inv_n / k);
+      *token_count = n_live;
+    }
+  } else {
+    finish_loss(t < E ? wsum[0][t] : 0.0, t < E ? hist[t] : 0, n_live, E, k, coef, loss, counts,
+                probs, token_count, red);
+  }
 }
 
-// One block adds the partial sums of n_parts blocks, in block order inside
-// each of the S = 1024 / E_pad slices and then slice by slice.
+// One block adds the partial sums of n_parts blocks: thread (s, q) those of
+// experts 4q .. 4q+3 from blocks s, s + S, ... in order (16-byte loads, S as
+// large as 1024 threads allow, so that a slice is a few loads in flight at
+// once), then the S slices in order.
 __global__ __launch_bounds__(1024) void balance_finish_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-    const int32_t* __restrict__ part_n, int n_parts, int E, int e_pad, int k, float coef,
+    const int32_t* __restrict__ part_n, int n_parts, int E, int quads, int k, float coef,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ probs,
     int32_t* __restrict__ token_count) {
-  __shared__ double sp[1024];
-  __shared__ int sc[1024];
+  __shared__ __attribute__((aligned(16))) double sp[4096];
+  __shared__ __attribute__((aligned(16))) int sc[4096];
   __shared__ double red[16];
-  __shared__ int n_live;
-  const int t = threadIdx.x, e = t % e_pad, s = t / e_pad, S = 1024 / e_pad;
-  if (t == 0) n_live = 0;
-  __syncthreads();
-  double p = 0.0;
-  int c = 0;
-  if (e < E) {
-#pragma unroll 8
+  __shared__ int live[16];
+  const int t = threadIdx.x, q = t % quads, s = t / quads, S = 1024 / quads;
+  const int e4 = (E + 3) & ~3;
+  int n = t < n_parts ? part_n[t] : 0;  // n_parts <= 1024
+  double p[4] = {0, 0, 0, 0};
+  int c[4] = {0, 0, 0, 0};
+  if (4 * q < E) {
+#pragma unroll 4
     for (int b = s; b < n_parts; b += S) {
-      p += part_p[(size_t)b * E + e];
-      c += part_c[(size_t)b * E + e];
+      const size_t o = (size_t)b * e4 + 4 * q;
+      const f32x4 pv = *reinterpret_cast<const f32x4*>(part_p + o);
+      const i32x4 cv = *reinterpret_cast<const i32x4*>(part_c + o);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        p[i] += pv[i];
+        c[i] += cv[i];
+      }
     }
   }
-  sp[t] = p;
-  sc[t] = c;
-  for (int b = t; b < n_parts; b += 1024) atomicAdd(&n_live, part_n[b]);
-  __syncthreads();
-  if (t < e_pad) {
-    for (int q = 1; q < S; q++) {
-      p += sp[q * e_pad + t];
-      c += sc[q * e_pad + t];
-    }
-    sp[t] = p;
-    sc[t] = c;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {  // expert 4q + i of slice s
+    sp[s * 4 * quads + 4 * q + i] = p[i];
+    sc[s * 4 * quads + 4 * q + i] = c[i];
   }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+  if (lane_id() == 0) live[t / kWave] = n;
   __syncthreads();
-  finish_loss(sp, sc, n_live, E, k, coef, loss, counts, probs, token_count, red);
+  double tp = 0.0;
+  int tc = 0;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < 16; w++) n += live[w];
+  if (t < E) {
+#pragma unroll 4
+    for (int x = 0; x < S; x++) {
+      tp += sp[x * 4 * quads + t];
+      tc += sc[x * 4 * quads + t];
+    }
+  }
+  finish_loss(tp, tc, n, E, k, coef, loss, counts, probs, token_count, red);
 }
 
 // Gradient rows.  SOFT: the row's softmax is needed (the balance term, or the
@@ -251,8 +334,14 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     const int32_t* __restrict__ token_count, const float* __restrict__ grad_loss, float coef,
     int renorm, int T, int E, int k, float* __restrict__ grad) {
   constexpr int N = 4 * NC, E_MAX = N * kRowLanes, ROWS = kGradThreads / kRowLanes;
-  __shared__ float sel[GATE ? ROWS : 1][GATE ? E_MAX : 1];
+  __shared__ __attribute__((aligned(16))) float sel[GATE ? ROWS : 1][GATE ? E_MAX : 4];
   const int t = threadIdx.x, l = t % kRowLanes, g = t / kRowLanes;
+  const long step = (long)gridDim.x * ROWS;
+  long r = (long)blockIdx.x * ROWS + g;
+  // the first row is on its way while the counts are turned into d
+  float v[N], v2[N];
+  bool on = row_live(mask, r, T);
+  if (SOFT && on) load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
   float d[N];
   float scale = 0.f;
   if (SOFT && grad_loss) {
@@ -260,42 +349,50 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     const double nk = (double)n * k, inv = n > 0 ? 1.0 / (nk * E) : 0.0;
     scale = n > 0 ? (float)((double)coef * E * *grad_loss / n) : 0.f;
 #pragma unroll
-    for (int c = 0; c < NC; c++)
+    for (int c = 0; c < NC; c++) {
+      i32x4 cv = {0, 0, 0, 0};
+      if (VEC) {
+        const int e = expert_of<true>(c, 0, l);
+        if (e < E) cv = *reinterpret_cast<const i32x4*>(counts + e);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const int e = expert_of<VEC>(c, i, l);
-        d[4 * c + i] = e < E ? (float)(((double)counts[e] * E - nk) * inv) : 0.f;
+        for (int i = 0; i < 4; i++) {
+          const int e = expert_of<false>(c, i, l);
+          if (e < E) cv[i] = counts[e];
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 4; i++) d[4 * c + i] = (float)(((double)cv[i] * E - nk) * inv);
+    }
   } else {
 #pragma unroll
     for (int q = 0; q < N; q++) d[q] = 0.f;
   }
   if (GATE) {
-    for (int e = l; e < E_MAX; e += kRowLanes) sel[g][e] = 0.f;
-    __syncthreads();
-  }
-  // every thread takes the same number of rounds (the block's rows may run out)
-  for (int r0 = blockIdx.x * ROWS; r0 < T; r0 += gridDim.x * ROWS) {
-    const int r = r0 + g;
-    const bool live = r < T && (!mask || mask[r]);
-    float v[N];
 #pragma unroll
-    for (int q = 0; q < N; q++) v[q] = 0.f;
+    for (int q = 0; q < N; q++) sel[g][q * kRowLanes + l] = 0.f;
+    wave_lds_fence();
+  }
+  // a wave's four rows take the same number of rounds: the LDS copy needs
+  // fences inside the wave only
+  auto round = [&](float(&v)[N], float(&next)[N]) {
+    const bool on1 = row_live(mask, r + step, T);
+    if (SOFT && on1) load_row<NC, VEC>(logits + (size_t)(r + step) * E, E, l, next, -INFINITY);
     float S = 0.f;
     int id = -1;
     if (GATE) {
       float wg = 0.f, wj = 0.f;
-      if (live && l < k) {
+      if (on && l < k) {
         const size_t f = (size_t)r * k + l;
         id = ids[f];
         wj = weights[f];
+        const float gj = grad_weights[f];
         wj = wj == wj ? wj : 0.f;  // the gating of a row without a finite logit
+        wg = wj * gj;
         if ((unsigned)id >= (unsigned)E) {
           id = -1;
-          wj = 0.f;
+          wj = wg = 0.f;
         }
-        wg = wj * grad_weights[f];
-        if (id < 0) wg = 0.f;
       }
       S = row_sum(wg);
       const float term = renorm ? wg - wj * S : wg;
@@ -310,11 +407,10 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
         }
       }
       if (first) sel[g][id] = sum;
-      __syncthreads();
+      wave_lds_fence();
     }
-    if (live) {
+    if (on) {
       if (SOFT) {
-        load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
         softmax_row(v);
         float dp = 0.f;
 #pragma unroll
@@ -326,10 +422,21 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
       }
       if (GATE) {
 #pragma unroll
-        for (int c = 0; c < NC; c++)
+        for (int c = 0; c < NC; c++) {
+          if (VEC) {
+            const f32x4 a = *reinterpret_cast<const f32x4*>(&sel[g][expert_of<true>(c, 0, l)]);
 #pragma unroll
-          for (int i = 0; i < 4; i++) v[4 * c + i] += sel[g][expert_of<VEC>(c, i, l)];
+            for (int i = 0; i < 4; i++) v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + a[i];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + sel[g][expert_of<false>(c, i, l)];
+          }
+        }
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < N; q++) v[q] = 0.f;
     }
     if (r < T) {
       float* out = grad + (size_t)r * E;
@@ -350,10 +457,16 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
       }
     }
     if (GATE) {
-      __syncthreads();  // the row's reads are done
+      wave_lds_fence();  // the row's reads are done
       if (id >= 0) sel[g][id] = 0.f;
-      __syncthreads();
+      wave_lds_fence();
     }
+    on = on1;
+    r += step;
+  };
+  while (r - (g & 3) < T) {  // the next row is on its way while one is worked on
+    round(v, v2);
+    round(v2, v);  // past the last row: nothing is read or written
   }
 }
 
@@ -387,16 +500,16 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const ui
                                int32_t* part_n, hipStream_t st) {
   const int nb = balance_loss_blocks(T), rows = (T + nb - 1) / nb;
 #define MOE_LOSS(NC_, VEC_)                                                                    \
-  balance_loss_kernel<NC_, VEC_><<<nb, kLossThreads, 0, st>>>(                                 \
+  balance_loss_kernel<NC_, VEC_><<<nb, loss_threads(NC_), 0, st>>>(                                 \
       logits, ids, mask, T, E, k, rows, coef, part_p, part_c, part_n, loss, counts, probs,     \
       token_count)
   MOE_BY_EXPERTS(MOE_LOSS);
 #undef MOE_LOSS
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || nb == 1) return err;
-  int e_pad = 1;
-  while (e_pad < E) e_pad *= 2;
-  balance_finish_kernel<<<1, 1024, 0, st>>>(part_p, part_c, part_n, nb, E, e_pad, k, coef, loss,
+  int quads = 1;
+  while (4 * quads < E) quads *= 2;
+  balance_finish_kernel<<<1, 1024, 0, st>>>(part_p, part_c, part_n, nb, E, quads, k, coef, loss,
                                             counts, probs, token_count);
   return hipGetLastError();
 }
