@@ -55,7 +55,10 @@ struct Layout {
 inline bool use_tiles(const moe_shape& s) {
   return s.wdtype != MOE_F32 && (long)s.T * s.k >= 16L * s.E;
 }
-inline int tiles_bm(const moe_shape& s) { return (long)s.T * s.k < 64L * s.E ? 64 : 128; }
+inline int tiles_bm(const moe_shape& s) {
+  if (s.wdtype == MOE_INT8 && (long)s.T * s.k >= 256L * s.E) return 256;
+  return (long)s.T * s.k < 64L * s.E ? 64 : 128;
+}
 
 // Grouping kernels by pair count, the same for the fused entry point and for
 // moe_align_sort: one block (gating or given ids, grouping, the tile list, and

@@ -1,0 +1,368 @@
+// gemm_i8_large.hip -- grouped int8 expert products for experts that hold
+// hundreds of pairs each.
+#include "moe_common.h"
+
+namespace moe {
+
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kLargeRows = 256;  // weight rows per block
+constexpr int kLargeK = 128;     // codes of K per stage
+constexpr int kABytes = kLargeRows * kLargeK;
+
+__device__ __forceinline__ int swz_l(int r) { return (r ^ (r >> 3)) & 7; }
+
+__device__ __forceinline__ void dma16(const char* src, char* dst) {
+  __builtin_amdgcn_global_load_lds(
+      (const __attribute__((address_space(1))) void*)src,
+      (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+// s_waitcnt with only vmcnt limited to 0 / only lgkmcnt limited to 0
+__device__ __forceinline__ void wait_vm0() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xc07f); }
+
+// RT x CT tiles of 32 x 32 per wave; WR x WC waves.
+template <int NPOS, int WR, int WC, int RT, int CT>
+__device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&bp)[NPOS / 32],
+                                           int n_stages, char* __restrict__ b0,
+                                           char* __restrict__ b1, i32x16 (&acc)[RT][CT]) {
+  const int lane = lane_id(), w = threadIdx.x / kWave;
+  const int r32 = lane & 31, hi = lane >> 5;
+  const int wr = w / WC, wc = w % WC;
+  constexpr int NB = NPOS / 32;
+  auto issue = [&](char* buf, int inc) {  // the next stage inc bytes further
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      dma16(ap[i], buf + (w * 8 + i) * 1024);
+      ap[i] += inc;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; i++) {
+      dma16(bp[i], buf + kABytes + (w * NB + i) * 1024);
+      bp[i] += inc;
+    }
+  };
+  // K step kk of tile i: chunk 2 kk + lane / 32 of row 32 i + r32, kept at
+  // slot chunk ^ swz(row); swz(row + 32 i) = swz(row) ^ 4 (i % 2), so every
+  // address is one of four (kk ^ 2 (i % 2)) plus a constant
+  const int rowa = wr * RT * 32 + r32, rowb = wc * CT * 32 + r32;
+  const int la = rowa * kLargeK + ((hi ^ swz_l(rowa)) << 4);
+  const int lb = kABytes + rowb * kLargeK + ((hi ^ swz_l(rowb)) << 4);
+  i32x4 fa[2][RT], fb[2][CT];
+  auto read = [&](const char* buf, int kk, i32x4(&a)[RT], i32x4(&b)[CT]) {
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+      a[i] = *reinterpret_cast<const i32x4*>(buf + (la ^ ((kk ^ (2 * (i & 1))) << 5)) + i * 4096);
+#pragma unroll
+    for (int i = 0; i < CT; i++)
+      b[i] = *reinterpret_cast<const i32x4*>(buf + (lb ^ ((kk ^ (2 * (i & 1))) << 5)) + i * 4096);
+  };
+  auto mma = [&](const i32x4(&a)[RT], const i32x4(&b)[CT]) {
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+      for (int j = 0; j < CT; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+  };
+  const int last = n_stages - 1;
+  issue(b0, last > 0 ? kLargeK : 0);
+  wait_vm0();
+  __builtin_amdgcn_s_barrier();
+  issue(b1, last > 1 ? kLargeK : 0);
+  read(b0, 0, fa[0], fb[0]);
+  // stage s in cur, s + 1 on its way to (or in) nxt
+  auto stage = [&](char* cur, char* nxt, int s) {
+#pragma unroll
+    for (int kk = 0; kk < 3; kk++) {
+      read(cur, kk + 1, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
+      mma(fa[kk & 1], fb[kk & 1]);
+#pragma unroll
+      for (int q = 0; q < RT + CT; q++) {
+        __builtin_amdgcn_sched_group_barrier(0x008, RT * CT / (RT + CT), 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    wait_lgkm0();
+    wait_vm0();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    read(nxt, 0, fa[0], fb[0]);
+    issue(cur, s + 2 < last ? kLargeK : 0);
+    mma(fa[1], fb[1]);
+#pragma unroll
+    for (int q = 0; q < RT + CT; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    }
+#pragma unroll
+    for (int q = 0; q < RT * CT - RT - CT; q++) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int s = 0;
+  for (; s + 2 <= n_stages; s += 2) {
+    stage(b0, b1, s);
+    stage(b1, b0, s + 1);
+  }
+  if (s < n_stages) stage(b0, b1, s);
+  // the last loads into LDS land, and every wave is done with its fragments:
+  // LDS is free for the epilogue
+  wait_lgkm0();
+  wait_vm0();
+  __builtin_amdgcn_s_barrier();
+}
+
+template <int NPOS>
+struct LargeShape;
+template <>
+struct LargeShape<256> {
+  static constexpr int WR = 2, WC = 2, RT = 4, CT = 4;
+};
+template <>
+struct LargeShape<128> {
+  static constexpr int WR = 4, WC = 1, RT = 2, CT = 4;
+};
+
+// LDS: two stage buffers of (256 + 256) rows of 128 bytes, then the block's
+// 256 channel scales and 256 row scales.  The epilogue lays the output tile
+// over the stage buffers, a row of 16-byte chunks per position with chunk c
+// of row p at slot c ^ (p mod the row's chunks), and stores whole lines.
+struct LargeLds {
+  char buf[4 * kABytes];
+  float ws[kLargeRows], as[256];
+};
+
+// bf16 of two floats (round to nearest even), the first in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b});
+}
+
+// Rows p < mt of CH chunks each from LDS to out, `pitch` bytes apart.
+template <int CH>
+__device__ __forceinline__ void store_rows(const char* buf, int mt, char* out, size_t pitch) {
+  for (int i = threadIdx.x; i < mt * CH; i += 256) {
+    const int p = i / CH, c = i % CH;
+    *reinterpret_cast<uint4*>(out + p * pitch + c * 16) =
+        *reinterpret_cast<const uint4*>(buf + p * CH * 16 + ((c ^ (p & (CH - 1))) << 4));
+  }
+}
+
+template <int NPOS>
+__device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
+                                               const float* w13_scale, const int32_t* sorted_ids,
+                                               const Tile& tl, int nb, int H, int I, int k,
+                                               const float* xs, uint16_t* h, LargeLds& L) {
+  typedef LargeShape<NPOS> S;
+  const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
+  const char* ap[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int r = (w * 8 + i) * 8 + (lane >> 3);
+    const int f = nb * 128 + (r >> 1);
+    const int row = (r & 1) ? I + f : f;
+    ap[i] = w13 + ((size_t)tl.e * 2 * I + row) * H + (((lane & 7) ^ swz_l(r)) << 4);
+  }
+  const char* bp[NPOS / 32];
+#pragma unroll
+  for (int i = 0; i < NPOS / 32; i++) {
+    const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
+    const int tok = sorted_ids[tl.p0 + min(r, tl.mt - 1)] / k;
+    bp[i] = b + (size_t)tok * H + (((lane & 7) ^ swz_l(r)) << 4);
+  }
+  L.ws[t] = w13_scale[(size_t)tl.e * 2 * I + (t & 1 ? I : 0) + nb * 128 + (t >> 1)];
+  if (t < NPOS) L.as[t] = xs[sorted_ids[tl.p0 + min(t, tl.mt - 1)] / k];
+  i32x16 acc[S::RT][S::CT];
+#pragma unroll
+  for (int i = 0; i < S::RT; i++)
+#pragma unroll
+    for (int j = 0; j < S::CT; j++)
+#pragma unroll
+      for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
+  large_loop<NPOS, S::WR, S::WC, S::RT, S::CT>(ap, bp, H / kLargeK, L.buf, L.buf + 2 * kABytes,
+                                               acc);
+  const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
+  float sx[S::CT];
+#pragma unroll
+  for (int j = 0; j < S::CT; j++) sx[j] = L.as[(wc * S::CT + j) * 32 + r32];
+#pragma unroll
+  for (int i = 0; i < S::RT; i++)
+#pragma unroll
+    for (int q = 0; q < 4; q++) {
+      const int r = (wr * S::RT + i) * 32 + q * 8 + hi * 4;  // rows r .. r + 3: g u g u
+      const f32x4 ws = *reinterpret_cast<const f32x4*>(&L.ws[r]);
+      const float l0 = ws[0] * -1.44269502f, l1 = ws[2] * -1.44269502f;
+#pragma unroll
+      for (int j = 0; j < S::CT; j++) {
+        float hv[2];
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+          const float ag = (float)acc[i][j][4 * q + 2 * u];
+          const float g = ag * (sx[j] * ws[2 * u]);
+          const float up = (float)acc[i][j][4 * q + 2 * u + 1] * (sx[j] * ws[2 * u + 1]);
+          // silu: e^-g = 2^(-g log2 e), the factor folded into the scale
+          const float e = __builtin_amdgcn_exp2f(ag * (sx[j] * (u ? l1 : l0)));
+          hv[u] = g * __builtin_amdgcn_rcpf(1.0f + e) * up;
+        }
+        const int p = (wc * S::CT + j) * 32 + r32;
+        *reinterpret_cast<uint32_t*>(L.buf + p * 256 + (((r >> 4) ^ (p & 15)) << 4) +
+                                     (r & 15)) = pack_bf16(hv[0], hv[1]);
+      }
+    }
+  __syncthreads();
+  store_rows<16>(L.buf, tl.mt, reinterpret_cast<char*>(h + (size_t)tl.p0 * I + nb * 128),
+                 (size_t)I * 2);
+}
+
+template <int NPOS, bool YB>
+__device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, const float* w2_scale,
+                                              const Tile& tl, int nb, int H, int I,
+                                              const float* hs, void* y, LargeLds& L) {
+  typedef LargeShape<NPOS> S;
+  const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
+  const char* ap[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const int r = (w * 8 + i) * 8 + (lane >> 3);
+    const int row = min(nb * kLargeRows + r, H - 1);
+    ap[i] = w2 + ((size_t)tl.e * H + row) * I + (((lane & 7) ^ swz_l(r)) << 4);
+  }
+  const char* bp[NPOS / 32];
+#pragma unroll
+  for (int i = 0; i < NPOS / 32; i++) {
+    const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
+    bp[i] = b + (size_t)(tl.p0 + min(r, tl.mt - 1)) * I + (((lane & 7) ^ swz_l(r)) << 4);
+  }
+  L.ws[t] = w2_scale[(size_t)tl.e * H + min(nb * kLargeRows + t, H - 1)];
+  if (t < NPOS) L.as[t] = hs[tl.p0 + min(t, tl.mt - 1)];
+  i32x16 acc[S::RT][S::CT];
+#pragma unroll
+  for (int i = 0; i < S::RT; i++)
+#pragma unroll
+    for (int j = 0; j < S::CT; j++)
+#pragma unroll
+      for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
+  large_loop<NPOS, S::WR, S::WC, S::RT, S::CT>(ap, bp, I / kLargeK, L.buf, L.buf + 2 * kABytes,
+                                               acc);
+  const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
+  float sh[S::CT];
+#pragma unroll
+  for (int j = 0; j < S::CT; j++) sh[j] = L.as[(wc * S::CT + j) * 32 + r32];
+  // a position's row in LDS holds 512 bytes: 256 channels in bf16, or in two
+  // passes 128 in fp32 (half of each wave's row tiles)
+  constexpr int PASSES = YB ? 1 : 2, RP = S::RT / PASSES, ES = YB ? 2 : 4;
+#pragma unroll
+  for (int pass = 0; pass < PASSES; pass++) {
+    if (pass) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RP; i++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int r = (wr * S::RT + pass * RP + i) * 32 + q * 8 + hi * 4;
+        const int o = ((wr * RP + i) * 32 + q * 8 + hi * 4) * ES;  // byte in the LDS row
+        const f32x4 ws = *reinterpret_cast<const f32x4*>(&L.ws[r]);
+#pragma unroll
+        for (int j = 0; j < S::CT; j++) {
+          float v[4];
+#pragma unroll
+          for (int u = 0; u < 4; u++)
+            v[u] = (float)acc[pass * RP + i][j][4 * q + u] * (ws[u] * sh[j]);
+          const int p = (wc * S::CT + j) * 32 + r32;
+          char* dst = L.buf + p * 512 + (((o >> 4) ^ (p & 31)) << 4) + (o & 15);
+          if (YB)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+          else
+            *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+        }
+      }
+    __syncthreads();
+    // segments of RP * 32 channels per wave row
+    constexpr int SEG = RP * 32 * ES / 16;  // chunks
+    for (int i = t; i < tl.mt * 32; i += 256) {
+      const int p = i / 32, c = i % 32;
+      const int ch = nb * kLargeRows + (c / SEG * S::RT + pass * RP) * 32 + c % SEG * 16 / ES;
+      if (ch < H)
+        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(y) +
+                                  ((size_t)(tl.p0 + p) * H + ch) * ES) =
+            *reinterpret_cast<const uint4*>(L.buf + p * 512 + ((c ^ (p & 31)) << 4));
+    }
+  }
+}
+
+// Block -> (tile, row block): XCD x = b % 8 takes the row blocks x, x + 8, ...;
+// kTileGroup consecutive tiles share a row block before the next one.
+constexpr int kTileGroup = 4;
+__device__ __forceinline__ bool large_work(int n_tiles, int n_blk, int* tile, int* nb) {
+  const int x = blockIdx.x % 8, s = blockIdx.x / 8, per = (n_blk + 7) / 8;
+  const int grp = s / (per * kTileGroup), rem = s - grp * per * kTileGroup;
+  *nb = rem / kTileGroup * 8 + x;
+  *tile = grp * kTileGroup + rem % kTileGroup;
+  return *tile < n_tiles && *nb < n_blk;
+}
+
+__global__ __launch_bounds__(256)
+__attribute__((amdgpu_waves_per_eu(1, 1))) void w13_large_i8(
+    const char* __restrict__ b, const char* __restrict__ w13, const float* __restrict__ w13_scale,
+    const int32_t* __restrict__ sorted_ids, const Tile* __restrict__ tiles,
+    const int32_t* __restrict__ num_tiles, int H, int I, int k, const float* __restrict__ xs,
+    uint16_t* __restrict__ h) {
+  __shared__ __attribute__((aligned(16))) LargeLds L;
+  int tile, nb;
+  if (!large_work(*num_tiles, I / 128, &tile, &nb)) return;
+  const Tile tl = tiles[tile];
+  if (tl.mt <= 128)
+    w13_large_tile<128>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
+  else
+    w13_large_tile<256>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
+}
+
+template <bool YB>
+__global__ __launch_bounds__(256)
+__attribute__((amdgpu_waves_per_eu(1, 1))) void w2_large_i8(
+    const char* __restrict__ b, const char* __restrict__ w2, const float* __restrict__ w2_scale,
+    const Tile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int H, int I,
+    const float* __restrict__ hs, void* __restrict__ y) {
+  __shared__ __attribute__((aligned(16))) LargeLds L;
+  int tile, nb;
+  if (!large_work(*num_tiles, (H + kLargeRows - 1) / kLargeRows, &tile, &nb)) return;
+  const Tile tl = tiles[tile];
+  if (tl.mt <= 128)
+    w2_large_tile<128, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+  else
+    w2_large_tile<256, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+}
+
+static long large_grid(long max_tiles, long n_blk) {
+  const long groups = (max_tiles + kTileGroup - 1) / kTileGroup;
+  return groups * kTileGroup * ((n_blk + 7) / 8) * 8;
+}
+
+hipError_t launch_w13_large_i8(const void* b, const void* w13, const float* w13_scale,
+                               const int32_t* sorted_ids, const Tile* tiles,
+                               const int32_t* num_tiles, int max_tiles, int H, int I, int k,
+                               const float* xs, void* h, hipEvent_t e0, hipEvent_t e1,
+                               hipStream_t st) {
+  launch_on(w13_large_i8, dim3(large_grid(max_tiles, I / 128)), dim3(256), st, e0, e1,
+            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w13), w13_scale,
+            sorted_ids, tiles, num_tiles, H, I, k, xs, reinterpret_cast<uint16_t*>(h));
+  return hipGetLastError();
+}
+
+hipError_t launch_w2_large_i8(const void* b, const void* w2, const float* w2_scale,
+                              const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
+                              int I, const float* hs, void* y, bool y_bf16, hipEvent_t e0,
+                              hipEvent_t e1, hipStream_t st) {
+  const dim3 grid(large_grid(max_tiles, (H + kLargeRows - 1) / kLargeRows));
+  launch_on(y_bf16 ? w2_large_i8<true> : w2_large_i8<false>, grid, dim3(256), st, e0, e1,
+            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w2), w2_scale, tiles,
+            num_tiles, H, I, hs, y);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -159,10 +159,12 @@ def w2_i8(h, w2, w2_scale, offsets):
 
 def w13_i8(x, w13, w13_scale, sorted_ids, offsets, k):
     """h [P,I] before its rounding to bf16, and the bound with it: g and u
-    carry 3 U; the exponential's argument turns that into 3 U |g|, expf adds
+    carry 3 U; the exponential's argument carries at most 4 U |g| (its factor
+    log2 e may round once more), the exponential adds
     4 U, the sum, quotient and product one U each (two for the quotient).
-    Past -g = 88.72 = 128 ln 2 the fp32 exponential is infinite and h becomes
-    0, where |h| <= |g u| e^g <= |g u| 2^-128."""
+    Past -g = 126 ln 2 the reciprocal of 1 + e^-g is below 2^-126, the least
+    normal number, and may become 0 (past 128 ln 2 the exponential is infinite
+    and it does), where |h| <= |g u| e^g <= |g u| 2^-126."""
     codes, s = quant_i8(x)
     tok = np.asarray(sorted_ids) // k
     e = expert_of(offsets, tok.size)
@@ -172,6 +174,6 @@ def w13_i8(x, w13, w13_scale, sorted_ids, offsets, k):
     g, u = gu[:, :I], gu[:, I:]
     with np.errstate(over="ignore"):
         h = g / (1.0 + np.exp(-g)) * u
-    bound = np.abs(h) * (U_BF16 * 1.001 + (3 * np.minimum(np.abs(g), 104) + 16) * U) + \
-        np.abs(g * u) * 2.0 ** -128 + 2.0 ** -120
+    bound = np.abs(h) * (U_BF16 * 1.001 + (4 * np.minimum(np.abs(g), 104) + 16) * U) + \
+        np.abs(g * u) * 2.0 ** -126 + 2.0 ** -120
     return h, bound

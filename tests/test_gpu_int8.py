@@ -95,6 +95,12 @@ LAYERS = [
     ("tiles_128_odd_rows", 400, 128, 3, 1, 128, 0.5),
     ("chunked", 1100, 256, 16, 8, 128, 1.0),
     ("large_experts", 1500, 512, 2, 1, 768, 0.2),
+    # 256-position tiles (256 or more pairs per expert): odd and single stage
+    # counts, channels that are no multiple of 256, ragged, short and absent tiles
+    ("large_one_stage", 600, 128, 2, 1, 128, 0.5),
+    ("large_odd_stages", 1100, 384, 3, 2, 640, 1.0),
+    ("large_skewed", 2100, 256, 6, 2, 384, 2.5),
+    ("large_many_tiles", 4100, 256, 1, 1, 256, 0.0),
 ]
 
 
