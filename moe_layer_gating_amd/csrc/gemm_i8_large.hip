@@ -27,20 +27,18 @@ template <int NPOS, int WR, int WC, int RT, int CT>
 __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&bp)[NPOS / 32],
                                            int n_stages, char* __restrict__ b0,
                                            char* __restrict__ b1, i32x16 (&acc)[RT][CT]) {
-  const int lane = lane_id(), w = threadIdx.x / kWave;
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r32 = lane & 31, hi = lane >> 5;
   const int wr = w / WC, wc = w % WC;
   constexpr int NB = NPOS / 32;
-  auto issue = [&](char* buf, int inc) {  // the next stage inc bytes further
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      dma16(ap[i], buf + (w * 8 + i) * 1024);
-      ap[i] += inc;
-    }
-#pragma unroll
-    for (int i = 0; i < NB; i++) {
-      dma16(bp[i], buf + kABytes + (w * NB + i) * 1024);
-      bp[i] += inc;
+  // the q-th of a stage's 8 + NB loads; the next one reads inc bytes further
+  auto load = [&](char* buf, int q, int inc) {
+    if (q < 8) {
+      dma16(ap[q], buf + (w * 8 + q) * 1024);
+      ap[q] += inc;
+    } else if (q < 8 + NB) {
+      dma16(bp[q - 8], buf + kABytes + (w * NB + q - 8) * 1024);
+      bp[q - 8] += inc;
     }
   };
   // K step kk of tile i: chunk 2 kk + lane / 32 of row 32 i + r32, kept at
@@ -50,59 +48,52 @@ __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&b
   const int la = rowa * kLargeK + ((hi ^ swz_l(rowa)) << 4);
   const int lb = kABytes + rowb * kLargeK + ((hi ^ swz_l(rowb)) << 4);
   i32x4 fa[2][RT], fb[2][CT];
-  auto read = [&](const char* buf, int kk, i32x4(&a)[RT], i32x4(&b)[CT]) {
-#pragma unroll
-    for (int i = 0; i < RT; i++)
-      a[i] = *reinterpret_cast<const i32x4*>(buf + (la ^ ((kk ^ (2 * (i & 1))) << 5)) + i * 4096);
-#pragma unroll
-    for (int i = 0; i < CT; i++)
-      b[i] = *reinterpret_cast<const i32x4*>(buf + (lb ^ ((kk ^ (2 * (i & 1))) << 5)) + i * 4096);
+  auto read = [&](const char* buf, int kk, int q, i32x4(&a)[RT], i32x4(&b)[CT]) {
+    const int i = q < RT ? q : q - RT, sw = (kk ^ (2 * (i & 1))) << 5;
+    if (q < RT)
+      a[i] = *reinterpret_cast<const i32x4*>(buf + (la ^ sw) + i * 4096);
+    else
+      b[i] = *reinterpret_cast<const i32x4*>(buf + (lb ^ sw) + i * 4096);
   };
-  auto mma = [&](const i32x4(&a)[RT], const i32x4(&b)[CT]) {
-#pragma unroll
-    for (int i = 0; i < RT; i++)
-#pragma unroll
-      for (int j = 0; j < CT; j++)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+  auto mma = [&](int q, const i32x4(&a)[RT], const i32x4(&b)[CT]) {
+    const int i = q / CT, j = q % CT;
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
   };
   const int last = n_stages - 1;
-  issue(b0, last > 0 ? kLargeK : 0);
+#pragma unroll
+  for (int q = 0; q < 8 + NB; q++) load(b0, q, last > 0 ? kLargeK : 0);
   wait_vm0();
-  __builtin_amdgcn_s_barrier();
-  issue(b1, last > 1 ? kLargeK : 0);
-  read(b0, 0, fa[0], fb[0]);
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < 8 + NB; q++) load(b1, q, last > 1 ? kLargeK : 0);
+#pragma unroll
+  for (int q = 0; q < RT + CT; q++) read(b0, 0, q, fa[0], fb[0]);
   // stage s in cur, s + 1 on its way to (or in) nxt
+  // (the order of the instructions is fixed: each MFMA is followed by what can
+  // be issued in its shadow, a fragment read and a load)
+  constexpr int M = RT * CT, R = RT + CT;
   auto stage = [&](char* cur, char* nxt, int s) {
 #pragma unroll
     for (int kk = 0; kk < 3; kk++) {
-      read(cur, kk + 1, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
-      mma(fa[kk & 1], fb[kk & 1]);
 #pragma unroll
-      for (int q = 0; q < RT + CT; q++) {
-        __builtin_amdgcn_sched_group_barrier(0x008, RT * CT / (RT + CT), 0);
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      for (int q = 0; q < M; q++) {
+        mma(q, fa[kk & 1], fb[kk & 1]);
+        if (q < R) read(cur, kk + 1, q, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
     wait_lgkm0();
     wait_vm0();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    read(nxt, 0, fa[0], fb[0]);
-    issue(cur, s + 2 < last ? kLargeK : 0);
-    mma(fa[1], fb[1]);
+    const int inc = s + 2 < last ? kLargeK : 0;
 #pragma unroll
-    for (int q = 0; q < RT + CT; q++) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    for (int q = 0; q < 16; q++) {
+      if (q < M) mma(q, fa[1], fb[1]);
+      if (q < R) read(nxt, 0, q, fa[0], fb[0]);
+      load(cur, q, inc);
+      __builtin_amdgcn_sched_barrier(0);
     }
-#pragma unroll
-    for (int q = 0; q < RT * CT - RT - CT; q++) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
   };
   int s = 0;
   for (; s + 2 <= n_stages; s += 2) {
@@ -196,17 +187,14 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
     for (int q = 0; q < 4; q++) {
       const int r = (wr * S::RT + i) * 32 + q * 8 + hi * 4;  // rows r .. r + 3: g u g u
       const f32x4 ws = *reinterpret_cast<const f32x4*>(&L.ws[r]);
-      const float l0 = ws[0] * -1.44269502f, l1 = ws[2] * -1.44269502f;
 #pragma unroll
       for (int j = 0; j < S::CT; j++) {
         float hv[2];
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-          const float ag = (float)acc[i][j][4 * q + 2 * u];
-          const float g = ag * (sx[j] * ws[2 * u]);
+          const float g = (float)acc[i][j][4 * q + 2 * u] * (sx[j] * ws[2 * u]);
           const float up = (float)acc[i][j][4 * q + 2 * u + 1] * (sx[j] * ws[2 * u + 1]);
-          // silu: e^-g = 2^(-g log2 e), the factor folded into the scale
-          const float e = __builtin_amdgcn_exp2f(ag * (sx[j] * (u ? l1 : l0)));
+          const float e = __builtin_amdgcn_exp2f(g * -1.44269502f);
           hv[u] = g * __builtin_amdgcn_rcpf(1.0f + e) * up;
         }
         const int p = (wc * S::CT + j) * 32 + r32;
