@@ -283,14 +283,14 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
   }
 }
 
-// Block -> (tile, row block): XCD x = b % 8 takes the row blocks x, x + 8, ...;
-// kTileGroup consecutive tiles share a row block before the next one.
-constexpr int kTileGroup = 4;
+// Block -> (tile, row block): XCD x = b % 8 takes the row blocks x, x + 8, ...
+// of a tile, then those of the next one, so that its L2 holds one tile's rows
+// and an eighth of the expert's weights.  (2, 4, 8 and 16 tiles side by side on
+// a row block ran 0.6, 1.6, 3.5 and 4% slower on 8 experts of 2048 pairs.)
 __device__ __forceinline__ bool large_work(int n_tiles, int n_blk, int* tile, int* nb) {
   const int x = blockIdx.x % 8, s = blockIdx.x / 8, per = (n_blk + 7) / 8;
-  const int grp = s / (per * kTileGroup), rem = s - grp * per * kTileGroup;
-  *nb = rem / kTileGroup * 8 + x;
-  *tile = grp * kTileGroup + rem % kTileGroup;
+  *tile = s / per;
+  *nb = (s - *tile * per) * 8 + x;
   return *tile < n_tiles && *nb < n_blk;
 }
 
@@ -327,8 +327,7 @@ __attribute__((amdgpu_waves_per_eu(1, 1))) void w2_large_i8(
 }
 
 static long large_grid(long max_tiles, long n_blk) {
-  const long groups = (max_tiles + kTileGroup - 1) / kTileGroup;
-  return groups * kTileGroup * ((n_blk + 7) / 8) * 8;
+  return max_tiles * ((n_blk + 7) / 8) * 8;
 }
 
 hipError_t launch_w13_large_i8(const void* b, const void* w13, const float* w13_scale,
