@@ -56,7 +56,7 @@ inline bool use_tiles(const moe_shape& s) {
   return s.wdtype != MOE_F32 && (long)s.T * s.k >= 16L * s.E;
 }
 inline int tiles_bm(const moe_shape& s) {
-  if (s.wdtype == MOE_INT8 && (long)s.T * s.k >= 256L * s.E) return 256;
+  if (s.wdtype == MOE_INT8 && (long)s.T * s.k >= 64L * s.E) return 256;
   return (long)s.T * s.k < 64L * s.E ? 64 : 128;
 }
 

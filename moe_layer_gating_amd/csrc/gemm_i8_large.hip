@@ -1,5 +1,7 @@
 // gemm_i8_large.hip -- grouped int8 expert products for experts that hold
 // hundreds of pairs each.
+#include <type_traits>
+
 #include "moe_common.h"
 
 namespace moe {
@@ -18,25 +20,34 @@ __device__ __forceinline__ void dma16(const char* src, char* dst) {
       (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
 }
 
-// s_waitcnt with only vmcnt limited to 0 / only lgkmcnt limited to 0
-__device__ __forceinline__ void wait_vm0() { __builtin_amdgcn_s_waitcnt(0x0f70); }
+// s_waitcnt with only vmcnt limited, to N / only lgkmcnt limited, to 0
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N < 64, "vmcnt has six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | (N >> 4) << 14);
+}
 __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 
-// RT x CT tiles of 32 x 32 per wave; WR x WC waves.
-template <int NPOS, int WR, int WC, int RT, int CT>
+// Main loop of a block of 4 waves on 256 weight rows and NPOS positions: each
+// of the WR x WC waves accumulates RT x CT tiles of 32 x 32.  A stage is 128
+// bytes of K of every row, loaded straight into one of NBUF LDS buffers
+// (weights, then tokens).  ap, bp: this lane's source of each load.
+template <int NPOS, int NBUF, int WR, int WC, int RT, int CT>
 __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&bp)[NPOS / 32],
                                            int n_stages, char* __restrict__ b0,
-                                           char* __restrict__ b1, i32x16 (&acc)[RT][CT]) {
+                                           char* __restrict__ b1, char* __restrict__ b2,
+                                           i32x16 (&acc)[RT][CT]) {
+  static_assert(NBUF == 2 || NBUF == 3, "buffers");
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r32 = lane & 31, hi = lane >> 5;
   const int wr = w / WC, wc = w % WC;
-  constexpr int NB = NPOS / 32;
-  // the q-th of a stage's 8 + NB loads; the next one reads inc bytes further
+  constexpr int NB = NPOS / 32, NL = 8 + NB;
+  // the q-th of a stage's loads; the next one reads inc bytes further
   auto load = [&](char* buf, int q, int inc) {
     if (q < 8) {
       dma16(ap[q], buf + (w * 8 + q) * 1024);
       ap[q] += inc;
-    } else if (q < 8 + NB) {
+    } else if (q < NL) {
       dma16(bp[q - 8], buf + kABytes + (w * NB + q - 8) * 1024);
       bp[q - 8] += inc;
     }
@@ -61,34 +72,38 @@ __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&b
   };
   const int last = n_stages - 1;
 #pragma unroll
-  for (int q = 0; q < 8 + NB; q++) load(b0, q, last > 0 ? kLargeK : 0);
-  wait_vm0();
-  __syncthreads();
+  for (int n = 0; n < NBUF; n++)
 #pragma unroll
-  for (int q = 0; q < 8 + NB; q++) load(b1, q, last > 1 ? kLargeK : 0);
+    for (int q = 0; q < NL; q++) load(n == 0 ? b0 : n == 1 ? b1 : b2, q, last > n ? kLargeK : 0);
+  wait_vm<(NBUF - 1) * NL>();
+  wait_lgkm0();  // the scales that the caller has stored
+  __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int q = 0; q < RT + CT; q++) read(b0, 0, q, fa[0], fb[0]);
-  // stage s in cur, s + 1 on its way to (or in) nxt
-  // (the order of the instructions is fixed: each MFMA is followed by what can
-  // be issued in its shadow, a fragment read and a load)
-  constexpr int M = RT * CT, R = RT + CT;
+  // Stage s in cur; s + 1 .. s + NBUF - 1 are in the other buffers or on their
+  // way.  The barrier before the last K step finds every wave done reading
+  // cur, which takes stage s + NBUF, and stage s + 1 landed.  (The order of the
+  // instructions is fixed: each MFMA is followed by what can be issued in its
+  // shadow, a fragment read and a load.  Past the last stage the loads repeat
+  // it, so that the wait counts stay.)
+  constexpr int M = RT * CT, R = RT + CT, S3 = M > R ? M : R, S4 = S3 > NL ? S3 : NL;
   auto stage = [&](char* cur, char* nxt, int s) {
 #pragma unroll
     for (int kk = 0; kk < 3; kk++) {
 #pragma unroll
-      for (int q = 0; q < M; q++) {
-        mma(q, fa[kk & 1], fb[kk & 1]);
+      for (int q = 0; q < S3; q++) {
+        if (q < M) mma(q, fa[kk & 1], fb[kk & 1]);
         if (q < R) read(cur, kk + 1, q, fa[(kk + 1) & 1], fb[(kk + 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     wait_lgkm0();
-    wait_vm0();
+    wait_vm<(NBUF - 2) * NL>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    const int inc = s + 2 < last ? kLargeK : 0;
+    const int inc = s + NBUF < last ? kLargeK : 0;
 #pragma unroll
-    for (int q = 0; q < 16; q++) {
+    for (int q = 0; q < S4; q++) {
       if (q < M) mma(q, fa[1], fb[1]);
       if (q < R) read(nxt, 0, q, fa[0], fb[0]);
       load(cur, q, inc);
@@ -96,36 +111,53 @@ __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&b
     }
   };
   int s = 0;
-  for (; s + 2 <= n_stages; s += 2) {
-    stage(b0, b1, s);
-    stage(b1, b0, s + 1);
+  if constexpr (NBUF == 2) {
+    for (; s + 2 <= n_stages; s += 2) {
+      stage(b0, b1, s);
+      stage(b1, b0, s + 1);
+    }
+    if (s < n_stages) stage(b0, b1, s);
+  } else {
+    for (; s + 3 <= n_stages; s += 3) {
+      stage(b0, b1, s);
+      stage(b1, b2, s + 1);
+      stage(b2, b0, s + 2);
+    }
+    if (s < n_stages) stage(b0, b1, s);
+    if (s + 1 < n_stages) stage(b1, b2, s + 1);
   }
-  if (s < n_stages) stage(b0, b1, s);
   // the last loads into LDS land, and every wave is done with its fragments:
   // LDS is free for the epilogue
   wait_lgkm0();
-  wait_vm0();
+  wait_vm<0>();
   __builtin_amdgcn_s_barrier();
 }
 
 template <int NPOS>
-struct LargeShape;
+struct LargeShape {  // 128 positions and fewer: a wave per 64 rows
+  static constexpr int WR = 4, WC = 1, RT = 2, CT = NPOS / 32;
+};
 template <>
 struct LargeShape<256> {
   static constexpr int WR = 2, WC = 2, RT = 4, CT = 4;
 };
-template <>
-struct LargeShape<128> {
-  static constexpr int WR = 4, WC = 1, RT = 2, CT = 4;
-};
 
-// LDS: two stage buffers of (256 + 256) rows of 128 bytes, then the block's
-// 256 channel scales and 256 row scales.  The epilogue lays the output tile
+// LDS: NBUF stage buffers of (256 + NPOS) rows of 128 bytes (the kernel's
+// widest tiles decide their size), then the block's channel and row scales.  The epilogue lays the output tile
 // over the stage buffers, a row of 16-byte chunks per position with chunk c
 // of row p at slot c ^ (p mod the row's chunks), and stores whole lines.
+template <int NPOS>
+constexpr int large_stage_bytes() {
+  return kABytes + NPOS * kLargeK;
+}
+template <int NPOS>
+constexpr int large_bufs() {
+  return NPOS == 256 ? 2 : 3;
+}
+template <int BM>
 struct LargeLds {
-  char buf[4 * kABytes];
-  float ws[kLargeRows], as[256];
+  char buf[3 * large_stage_bytes<BM == 256 ? 128 : BM>()];
+  float ws[kLargeRows], as[BM];
 };
 
 // bf16 of two floats (round to nearest even), the first in the low half
@@ -144,11 +176,11 @@ __device__ __forceinline__ void store_rows(const char* buf, int mt, char* out, s
   }
 }
 
-template <int NPOS>
+template <int NPOS, int BM>
 __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
                                                const float* w13_scale, const int32_t* sorted_ids,
                                                const Tile& tl, int nb, int H, int I, int k,
-                                               const float* xs, uint16_t* h, LargeLds& L) {
+                                               const float* xs, uint16_t* h, LargeLds<BM>& L) {
   typedef LargeShape<NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
   const char* ap[8];
@@ -175,8 +207,10 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
     for (int j = 0; j < S::CT; j++)
 #pragma unroll
       for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
-  large_loop<NPOS, S::WR, S::WC, S::RT, S::CT>(ap, bp, H / kLargeK, L.buf, L.buf + 2 * kABytes,
-                                               acc);
+  constexpr int SB = large_stage_bytes<NPOS>();
+  static_assert(NPOS <= BM && large_bufs<NPOS>() * SB <= (int)sizeof(L.buf), "stage buffers");
+  large_loop<NPOS, large_bufs<NPOS>(), S::WR, S::WC, S::RT, S::CT>(ap, bp, H / kLargeK, L.buf, L.buf + SB,
+                                                        L.buf + 2 * SB, acc);
   const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
   float sx[S::CT];
 #pragma unroll
@@ -207,10 +241,10 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
                  (size_t)I * 2);
 }
 
-template <int NPOS, bool YB>
+template <int NPOS, int BM, bool YB>
 __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, const float* w2_scale,
                                               const Tile& tl, int nb, int H, int I,
-                                              const float* hs, void* y, LargeLds& L) {
+                                              const float* hs, void* y, LargeLds<BM>& L) {
   typedef LargeShape<NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
   const char* ap[8];
@@ -235,8 +269,10 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
     for (int j = 0; j < S::CT; j++)
 #pragma unroll
       for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
-  large_loop<NPOS, S::WR, S::WC, S::RT, S::CT>(ap, bp, I / kLargeK, L.buf, L.buf + 2 * kABytes,
-                                               acc);
+  constexpr int SB = large_stage_bytes<NPOS>();
+  static_assert(NPOS <= BM && large_bufs<NPOS>() * SB <= (int)sizeof(L.buf), "stage buffers");
+  large_loop<NPOS, large_bufs<NPOS>(), S::WR, S::WC, S::RT, S::CT>(ap, bp, I / kLargeK, L.buf, L.buf + SB,
+                                                        L.buf + 2 * SB, acc);
   const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
   float sh[S::CT];
 #pragma unroll
@@ -294,61 +330,72 @@ __device__ __forceinline__ bool large_work(int n_tiles, int n_blk, int* tile, in
   return *tile < n_tiles && *nb < n_blk;
 }
 
+// The narrowest main loop that holds a tile of mt positions.
+template <int BM, typename F>
+__device__ __forceinline__ void by_width(int mt, F&& run) {
+  if constexpr (BM == 256)
+    if (mt > 128) return run(std::integral_constant<int, 256>{});
+  if constexpr (BM >= 128)
+    if (mt > 64) return run(std::integral_constant<int, 128>{});
+  if (mt > 32) return run(std::integral_constant<int, 64>{});
+  run(std::integral_constant<int, 32>{});
+}
+
+template <int BM>
 __global__ __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(1, 1))) void w13_large_i8(
     const char* __restrict__ b, const char* __restrict__ w13, const float* __restrict__ w13_scale,
     const int32_t* __restrict__ sorted_ids, const Tile* __restrict__ tiles,
     const int32_t* __restrict__ num_tiles, int H, int I, int k, const float* __restrict__ xs,
     uint16_t* __restrict__ h) {
-  __shared__ __attribute__((aligned(16))) LargeLds L;
+  __shared__ __attribute__((aligned(16))) LargeLds<BM> L;
   int tile, nb;
   if (!large_work(*num_tiles, I / 128, &tile, &nb)) return;
   const Tile tl = tiles[tile];
-  if (tl.mt <= 128)
-    w13_large_tile<128>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
-  else
-    w13_large_tile<256>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
+  by_width<BM>(tl.mt, [&](auto n) {
+    w13_large_tile<n.value, BM>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
+  });
 }
 
-template <bool YB>
+template <int BM, bool YB>
 __global__ __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(1, 1))) void w2_large_i8(
     const char* __restrict__ b, const char* __restrict__ w2, const float* __restrict__ w2_scale,
     const Tile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int H, int I,
     const float* __restrict__ hs, void* __restrict__ y) {
-  __shared__ __attribute__((aligned(16))) LargeLds L;
+  __shared__ __attribute__((aligned(16))) LargeLds<BM> L;
   int tile, nb;
   if (!large_work(*num_tiles, (H + kLargeRows - 1) / kLargeRows, &tile, &nb)) return;
   const Tile tl = tiles[tile];
-  if (tl.mt <= 128)
-    w2_large_tile<128, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
-  else
-    w2_large_tile<256, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+  by_width<BM>(tl.mt, [&](auto n) {
+    w2_large_tile<n.value, BM, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+  });
 }
 
-static long large_grid(long max_tiles, long n_blk) {
-  return max_tiles * ((n_blk + 7) / 8) * 8;
-}
+static long large_grid(long max_tiles, long n_blk) { return max_tiles * ((n_blk + 7) / 8) * 8; }
 
-hipError_t launch_w13_large_i8(const void* b, const void* w13, const float* w13_scale,
+hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const float* w13_scale,
                                const int32_t* sorted_ids, const Tile* tiles,
                                const int32_t* num_tiles, int max_tiles, int H, int I, int k,
                                const float* xs, void* h, hipEvent_t e0, hipEvent_t e1,
                                hipStream_t st) {
-  launch_on(w13_large_i8, dim3(large_grid(max_tiles, I / 128)), dim3(256), st, e0, e1,
+  const auto kern = bm == 256 ? w13_large_i8<256> : bm == 128 ? w13_large_i8<128> : w13_large_i8<64>;
+  launch_on(kern, dim3(large_grid(max_tiles, I / 128)), dim3(256), st, e0, e1,
             reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w13), w13_scale,
             sorted_ids, tiles, num_tiles, H, I, k, xs, reinterpret_cast<uint16_t*>(h));
   return hipGetLastError();
 }
 
-hipError_t launch_w2_large_i8(const void* b, const void* w2, const float* w2_scale,
+hipError_t launch_w2_large_i8(int bm, const void* b, const void* w2, const float* w2_scale,
                               const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
                               int I, const float* hs, void* y, bool y_bf16, hipEvent_t e0,
                               hipEvent_t e1, hipStream_t st) {
   const dim3 grid(large_grid(max_tiles, (H + kLargeRows - 1) / kLargeRows));
-  launch_on(y_bf16 ? w2_large_i8<true> : w2_large_i8<false>, grid, dim3(256), st, e0, e1,
-            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w2), w2_scale, tiles,
-            num_tiles, H, I, hs, y);
+  const auto kern = bm == 256   ? (y_bf16 ? w2_large_i8<256, true> : w2_large_i8<256, false>)
+                    : bm == 128 ? (y_bf16 ? w2_large_i8<128, true> : w2_large_i8<128, false>)
+                                : (y_bf16 ? w2_large_i8<64, true> : w2_large_i8<64, false>);
+  launch_on(kern, grid, dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
+            reinterpret_cast<const char*>(w2), w2_scale, tiles, num_tiles, H, I, hs, y);
   return hipGetLastError();
 }
 

@@ -532,8 +532,8 @@ hipError_t launch_w13_tiles(int mode, int bm, const void* b, const void* w13,
 #define MOE_W13_TILES(MODE_, BM_)                                                             \
   launch_tiles_w13_mode<MODE_, BM_>(max_tiles, bb, ww, w13_scale, sorted_ids, tiles, num_tiles, \
                                     H, I, k, act_amax_bits, h, amax_h_bits, e0, e1, st)
-  if (mode == MOE_INT8 && bm == 256)
-    return launch_w13_large_i8(b, w13, w13_scale, sorted_ids, tiles, num_tiles, max_tiles, H, I, k,
+  if (mode == MOE_INT8)
+    return launch_w13_large_i8(bm, b, w13, w13_scale, sorted_ids, tiles, num_tiles, max_tiles, H, I, k,
                                reinterpret_cast<const float*>(act_amax_bits), h, e0, e1, st);
   if (mode == MOE_BF16 && bm == 64)
     MOE_W13_TILES(MOE_BF16, 64);
@@ -564,8 +564,8 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
   launch_tiles_w2_mode<MODE_, BM_, YB_>(max_tiles, bb, ww, w2_scale, tiles, num_tiles, H, I,    \
                                         act_amax_bits, y, e0, e1, st)
   if (y_bf16 && mode != MOE_FP8_E4M3 && mode != MOE_INT8) return hipErrorInvalidValue;
-  if (mode == MOE_INT8 && bm == 256)
-    return launch_w2_large_i8(b, w2, w2_scale, tiles, num_tiles, max_tiles, H, I,
+  if (mode == MOE_INT8)
+    return launch_w2_large_i8(bm, b, w2, w2_scale, tiles, num_tiles, max_tiles, H, I,
                               reinterpret_cast<const float*>(act_amax_bits), y, y_bf16, e0, e1, st);
   if (mode == MOE_BF16 && bm == 64)
     MOE_W2_TILES(MOE_BF16, 64, false);
