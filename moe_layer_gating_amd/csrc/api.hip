@@ -55,9 +55,17 @@ struct Layout {
 inline bool use_tiles(const moe_shape& s) {
   return s.wdtype != MOE_F32 && (long)s.T * s.k >= 16L * s.E;
 }
+// INT8: 256-position tiles (an expert of up to 256 pairs reads its weights
+// once) where the mean is 64 or more and about every CU gets one of their
+// gate/up blocks; below that 64-position tiles on half the rows, whose blocks
+// are an eighth.  Measured, both projections of one expert: 4096 pairs at H =
+// I = 4096 (544 blocks of the large tiles) 467 us in the small tiles against
+// 217 us; 1024 pairs at 2048 (80 blocks) 47 against 77 us.
 inline int tiles_bm(const moe_shape& s) {
-  if (s.wdtype == MOE_INT8 && (long)s.T * s.k >= 64L * s.E) return 256;
-  return (long)s.T * s.k < 64L * s.E ? 64 : 128;
+  const long np = (long)s.T * s.k;
+  if (s.wdtype == MOE_INT8)
+    return np >= 64L * s.E && (np / 256 + s.E) * (s.I / 128) >= 256 ? 256 : 64;
+  return np < 64L * s.E ? 64 : 128;
 }
 
 // Grouping kernels by pair count, the same for the fused entry point and for
@@ -320,21 +328,22 @@ int moe_grouped_gemm_w13_swiglu(const moe_shape* s, const void* x, const void* w
   Tile* tiles = at<Tile>(ws, L.tiles);
   Tile* tiles_big = at<Tile>(ws, L.tiles_big);
   const bool big = use_tiles(*s);
-  MOE_TRY(launch_zero_words(reinterpret_cast<uint32_t*>(ctrl), sizeof(Ctrl) / 4, st));
-  if (big)
-    MOE_TRY(launch_build_tiles(expert_offsets, s->E, tiles_bm(*s), tiles_big,
-                               &ctrl->num_tiles_big, st));
-  else
-    MOE_TRY(launch_build_tiles(expert_offsets, s->E, kSkinnyBM, tiles, &ctrl->num_tiles, st));
   const void* b = x;
   const uint32_t* act = &ctrl->amax_x_bits;
-  if (i8) {
-    int8_t* xq = at<int8_t>(ws, L.xq);
-    float* xs = at<float>(ws, L.xs);
-    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(x), s->T, s->H, xq, xs, st));
-    b = xq;
-    act = reinterpret_cast<const uint32_t*>(xs);
+  RowQuant rq{};
+  if (i8) {  // the rows' codes ride along with the tile list
+    rq = RowQuant{reinterpret_cast<const uint16_t*>(x), s->T, s->H / 8, at<int8_t>(ws, L.xq),
+                  at<float>(ws, L.xs)};
+    b = rq.codes;
+    act = reinterpret_cast<const uint32_t*>(rq.scales);
+  } else {
+    MOE_TRY(launch_zero_words(reinterpret_cast<uint32_t*>(ctrl), sizeof(Ctrl) / 4, st));
   }
+  if (big)
+    MOE_TRY(launch_build_tiles(expert_offsets, s->E, tiles_bm(*s), tiles_big,
+                               &ctrl->num_tiles_big, st, rq));
+  else
+    MOE_TRY(launch_build_tiles(expert_offsets, s->E, kSkinnyBM, tiles, &ctrl->num_tiles, st, rq));
   if (fp8) {
     uint8_t* xq = at<uint8_t>(ws, L.xq);
     if ((rc = enqueue_quant(reinterpret_cast<const uint16_t*>(x), (long)s->T * s->H,
@@ -373,11 +382,15 @@ int moe_grouped_gemm_w2(const moe_shape* s, const void* h, const void* w2, const
   Tile* tiles = at<Tile>(ws, L.tiles);
   Tile* tiles_big = at<Tile>(ws, L.tiles_big);
   const bool big = use_tiles(*s);
+  RowQuant rq{};
+  if (i8)
+    rq = RowQuant{reinterpret_cast<const uint16_t*>(h), (long)s->T * s->k, s->I / 8,
+                  at<int8_t>(ws, L.hq), at<float>(ws, L.hs)};
   if (big)
     MOE_TRY(launch_build_tiles(expert_offsets, s->E, tiles_bm(*s), tiles_big,
-                               &ctrl->num_tiles_big, st));
+                               &ctrl->num_tiles_big, st, rq));
   else
-    MOE_TRY(launch_build_tiles(expert_offsets, s->E, kSkinnyBM, tiles, &ctrl->num_tiles, st));
+    MOE_TRY(launch_build_tiles(expert_offsets, s->E, kSkinnyBM, tiles, &ctrl->num_tiles, st, rq));
   const void* b = h;
   // act_scales[3] holds amax(h) as an fp32 value; its bit pattern is what the
   // kernels read.
@@ -389,12 +402,8 @@ int moe_grouped_gemm_w2(const moe_shape* s, const void* h, const void* w2, const
     b = hq;
   }
   if (i8) {
-    int8_t* hq = at<int8_t>(ws, L.hq);
-    float* hs = at<float>(ws, L.hs);
-    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(h), (long)s->T * s->k, s->I, hq,
-                                 hs, st));
-    b = hq;
-    amax_h = reinterpret_cast<const uint32_t*>(hs);
+    b = rq.codes;
+    amax_h = reinterpret_cast<const uint32_t*>(rq.scales);
   }
   if (big)
     MOE_TRY(launch_w2_tiles(s->wdtype, tiles_bm(*s), b, w2, w2_scale, tiles_big,
@@ -427,8 +436,8 @@ int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, floa
   if (rows == 0) return MOE_OK;
   if (!a || !codes || !scales) return MOE_ERR_INVALID_ARG;
   if (!aligned16(a) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(a), (long)rows, n,
-                                         codes, scales, reinterpret_cast<hipStream_t>(stream)));
+  const RowQuant rq{reinterpret_cast<const uint16_t*>(a), (long)rows, n / 8, codes, scales};
+  return hip_status(launch_quant_i8_rows(rq, reinterpret_cast<hipStream_t>(stream)));
 }
 
 int moe_inv_rope_fp8_quant(const void* x, const int32_t* positions, const float* cos_sin,
@@ -672,12 +681,14 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
                       (long)T * k < 256L * E;
   Tile* tiles_w2 = spread ? at<Tile>(ws, L.tiles_spread) : tiles_big;
   MOE_TRY(mark(0));
+  // INT8: the codes of x ride along in extra blocks of the first launch (the
+  // front kernel or the gating), whose own work is latency-bound
+  RowQuant rq{};
   if (i8) {
-    int8_t* codes = at<int8_t>(ws, L.xq);
-    float* xs = at<float>(ws, L.xs);
-    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(x), T, H, codes, xs, st));
-    bx = codes;
-    act_x = reinterpret_cast<const uint32_t*>(xs);
+    rq = RowQuant{reinterpret_cast<const uint16_t*>(x), T, H / 8, at<int8_t>(ws, L.xq),
+                  at<float>(ws, L.xs)};
+    bx = rq.codes;
+    act_x = reinterpret_cast<const uint32_t*>(rq.scales);
   }
   if (grouping == Grouping::kOneBlock) {
     // the front kernel's second block quantises a small x; a large one goes
@@ -687,7 +698,7 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
                                offsets, sorted, inv, bm, big, tl, ctrl,
                                reinterpret_cast<const uint16_t*>(x), H,
                                front_quant ? xq : nullptr,
-                               reinterpret_cast<const uint16_t*>(wg), logits_out, st));
+                               reinterpret_cast<const uint16_t*>(wg), logits_out, st, rq));
     for (int i = 1; i <= 3; i++) MOE_TRY(mark(i));
     if (fp8 && !front_quant &&
         (rc = enqueue_quant(reinterpret_cast<const uint16_t*>(x), (long)T * H, &ctrl->amax_x_bits,
@@ -702,7 +713,7 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
     const XWork* xwp = fp8 ? &xw : nullptr;
     // zeroes the control block
     MOE_TRY(launch_topk_gating(logits, T, E, k, s->renormalize, ids, wts,
-                               reinterpret_cast<uint32_t*>(ctrl), sizeof(Ctrl) / 4, st, xwp));
+                               reinterpret_cast<uint32_t*>(ctrl), sizeof(Ctrl) / 4, st, xwp, rq));
     MOE_TRY(mark(1));
     int32_t* nt = big ? &ctrl->num_tiles_big : &ctrl->num_tiles;
     if (grouping == Grouping::kChunked) {
@@ -733,12 +744,11 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
     bh = hq;
   }
   if (i8) {
-    int8_t* codes = at<int8_t>(ws, L.hq);
-    float* hs = at<float>(ws, L.hs);
-    MOE_TRY(launch_quant_i8_rows(reinterpret_cast<const uint16_t*>(h), (long)T * k, I, codes, hs,
-                                 st));
-    bh = codes;
-    act_h = reinterpret_cast<const uint32_t*>(hs);
+    const RowQuant hq{reinterpret_cast<const uint16_t*>(h), (long)T * k, I / 8,
+                      at<int8_t>(ws, L.hq), at<float>(ws, L.hs)};
+    MOE_TRY(launch_quant_i8_rows(hq, st));
+    bh = hq.codes;
+    act_h = reinterpret_cast<const uint32_t*>(hq.scales);
   }
   // FP8 and INT8 layers with many tokens per expert keep y in bf16 between the down
   // projection and the aggregation (half the bytes of that round trip); the

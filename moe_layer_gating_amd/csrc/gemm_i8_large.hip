@@ -8,9 +8,7 @@ namespace moe {
 
 typedef int i32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kLargeRows = 256;  // weight rows per block
-constexpr int kLargeK = 128;     // codes of K per stage
-constexpr int kABytes = kLargeRows * kLargeK;
+constexpr int kLargeK = 128;  // codes of K per stage
 
 __device__ __forceinline__ int swz_l(int r) { return (r ^ (r >> 3)) & 7; }
 
@@ -28,28 +26,30 @@ __device__ __forceinline__ void wait_vm() {
 }
 __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xc07f); }
 
-// Main loop of a block of 4 waves on 256 weight rows and NPOS positions: each
+// Main loop of a block of 4 waves on ROWS weight rows and NPOS positions: each
 // of the WR x WC waves accumulates RT x CT tiles of 32 x 32.  A stage is 128
 // bytes of K of every row, loaded straight into one of NBUF LDS buffers
-// (weights, then tokens).  ap, bp: this lane's source of each load.
-template <int NPOS, int NBUF, int WR, int WC, int RT, int CT>
-__device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&bp)[NPOS / 32],
-                                           int n_stages, char* __restrict__ b0,
-                                           char* __restrict__ b1, char* __restrict__ b2,
-                                           i32x16 (&acc)[RT][CT]) {
+// (weights, then tokens).  ap: this lane's source of each weight load; tokens()
+// gives those of the token loads, called once the first weights are on their
+// way (it may wait for the rows' token numbers).
+template <int ROWS, int NPOS, int NBUF, int WR, int WC, int RT, int CT, typename Tokens>
+__device__ __forceinline__ void large_loop(const char* (&ap)[ROWS / 32], Tokens&& tokens, int n_stages,
+                                           char* __restrict__ b0, char* __restrict__ b1,
+                                           char* __restrict__ b2, i32x16 (&acc)[RT][CT]) {
   static_assert(NBUF == 2 || NBUF == 3, "buffers");
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r32 = lane & 31, hi = lane >> 5;
   const int wr = w / WC, wc = w % WC;
-  constexpr int NB = NPOS / 32, NL = 8 + NB;
+  constexpr int NA = ROWS / 32, NB = NPOS / 32, NL = NA + NB, kABytes = ROWS * kLargeK;
+  const char* bp[NB];
   // the q-th of a stage's loads; the next one reads inc bytes further
   auto load = [&](char* buf, int q, int inc) {
-    if (q < 8) {
-      dma16(ap[q], buf + (w * 8 + q) * 1024);
+    if (q < NA) {
+      dma16(ap[q], buf + (w * NA + q) * 1024);
       ap[q] += inc;
     } else if (q < NL) {
-      dma16(bp[q - 8], buf + kABytes + (w * NB + q - 8) * 1024);
-      bp[q - 8] += inc;
+      dma16(bp[q - NA], buf + kABytes + (w * NB + q - NA) * 1024);
+      bp[q - NA] += inc;
     }
   };
   // K step kk of tile i: chunk 2 kk + lane / 32 of row 32 i + r32, kept at
@@ -71,12 +71,18 @@ __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&b
     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
   };
   const int last = n_stages - 1;
+  // stage by stage: the waits below count the loads issued after a stage's
+  // (others in between only make them stricter)
 #pragma unroll
-  for (int n = 0; n < NBUF; n++)
+  for (int n = 0; n < NBUF; n++) {
 #pragma unroll
-    for (int q = 0; q < NL; q++) load(n == 0 ? b0 : n == 1 ? b1 : b2, q, last > n ? kLargeK : 0);
+    for (int q = 0; q < NL; q++) {
+      if (n == 0 && q == NA) tokens(bp);
+      load(n == 0 ? b0 : n == 1 ? b1 : b2, q, last > n ? kLargeK : 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
   wait_vm<(NBUF - 1) * NL>();
-  wait_lgkm0();  // the scales that the caller has stored
   __builtin_amdgcn_s_barrier();
 #pragma unroll
   for (int q = 0; q < RT + CT; q++) read(b0, 0, q, fa[0], fb[0]);
@@ -133,31 +139,30 @@ __device__ __forceinline__ void large_loop(const char* (&ap)[8], const char* (&b
   __builtin_amdgcn_s_barrier();
 }
 
-template <int NPOS>
-struct LargeShape {  // 128 positions and fewer: a wave per 64 rows
-  static constexpr int WR = 4, WC = 1, RT = 2, CT = NPOS / 32;
+// Waves and their tiles, LDS stages.  256 positions: 2 x 2 waves of 128 x 128
+// (the fewest fragment bytes per MFMA; 256 accumulators leave one wave per
+// SIMD); fewer: a wave per quarter of the rows.
+template <int ROWS, int NPOS>
+struct LargeShape {
+  static constexpr int NBUF = 3, WR = 4, WC = 1, RT = ROWS / 128, CT = NPOS / 32;
+  static constexpr int STAGE = (ROWS + NPOS) * kLargeK;
 };
 template <>
-struct LargeShape<256> {
-  static constexpr int WR = 2, WC = 2, RT = 4, CT = 4;
+struct LargeShape<256, 256> {
+  static constexpr int NBUF = 2, WR = 2, WC = 2, RT = 4, CT = 4;
+  static constexpr int STAGE = 512 * kLargeK;
 };
 
-// LDS: NBUF stage buffers of (256 + NPOS) rows of 128 bytes (the kernel's
-// widest tiles decide their size), then the block's channel and row scales.  The epilogue lays the output tile
+// LDS: NBUF stage buffers of (ROWS + NPOS) rows of 128 bytes (the kernel's
+// widest tiles decide their size), then the block's channel and row scales.
+// The epilogue lays the output tile
 // over the stage buffers, a row of 16-byte chunks per position with chunk c
 // of row p at slot c ^ (p mod the row's chunks), and stores whole lines.
-template <int NPOS>
-constexpr int large_stage_bytes() {
-  return kABytes + NPOS * kLargeK;
-}
-template <int NPOS>
-constexpr int large_bufs() {
-  return NPOS == 256 ? 2 : 3;
-}
-template <int BM>
+template <int ROWS, int BM>
 struct LargeLds {
-  char buf[3 * large_stage_bytes<BM == 256 ? 128 : BM>()];
-  float ws[kLargeRows], as[BM];
+  static constexpr int N = BM < 256 ? BM : 128;
+  char buf[LargeShape<ROWS, N>::NBUF * LargeShape<ROWS, N>::STAGE];
+  float ws[ROWS], as[BM];
 };
 
 // bf16 of two floats (round to nearest even), the first in the low half
@@ -176,30 +181,38 @@ __device__ __forceinline__ void store_rows(const char* buf, int mt, char* out, s
   }
 }
 
-template <int NPOS, int BM>
+template <int ROWS, int NPOS, int BM>
 __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
                                                const float* w13_scale, const int32_t* sorted_ids,
                                                const Tile& tl, int nb, int H, int I, int k,
-                                               const float* xs, uint16_t* h, LargeLds<BM>& L) {
-  typedef LargeShape<NPOS> S;
+                                               const float* xs, uint16_t* h, LargeLds<ROWS, BM>& L) {
+  typedef LargeShape<ROWS, NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
-  const char* ap[8];
+  constexpr int NA = ROWS / 32, F = ROWS / 2;  // weight loads of a lane, features
+  const char* ap[NA];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int r = (w * 8 + i) * 8 + (lane >> 3);
-    const int f = nb * 128 + (r >> 1);
+  for (int i = 0; i < NA; i++) {
+    const int r = (w * NA + i) * 8 + (lane >> 3);
+    const int f = nb * F + (r >> 1);
     const int row = (r & 1) ? I + f : f;
     ap[i] = w13 + ((size_t)tl.e * 2 * I + row) * H + (((lane & 7) ^ swz_l(r)) << 4);
   }
-  const char* bp[NPOS / 32];
+  int id[NPOS / 32], as_id = 0;
 #pragma unroll
-  for (int i = 0; i < NPOS / 32; i++) {
-    const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
-    const int tok = sorted_ids[tl.p0 + min(r, tl.mt - 1)] / k;
-    bp[i] = b + (size_t)tok * H + (((lane & 7) ^ swz_l(r)) << 4);
-  }
-  L.ws[t] = w13_scale[(size_t)tl.e * 2 * I + (t & 1 ? I : 0) + nb * 128 + (t >> 1)];
-  if (t < NPOS) L.as[t] = xs[sorted_ids[tl.p0 + min(t, tl.mt - 1)] / k];
+  for (int i = 0; i < NPOS / 32; i++)
+    id[i] = sorted_ids[tl.p0 + min((w * (NPOS / 32) + i) * 8 + (lane >> 3), tl.mt - 1)];
+  if (t < NPOS) as_id = sorted_ids[tl.p0 + min(t, tl.mt - 1)];
+  float as_t = 0.f;
+  auto tokens = [&](const char*(&bp)[NPOS / 32]) {
+#pragma unroll
+    for (int i = 0; i < NPOS / 32; i++) {
+      const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
+      bp[i] = b + (size_t)(id[i] / k) * H + (((lane & 7) ^ swz_l(r)) << 4);
+    }
+    if (t < NPOS) as_t = xs[as_id / k];
+  };
+  float ws_t = 0.f;
+  if (t < ROWS) ws_t = w13_scale[(size_t)tl.e * 2 * I + (t & 1 ? I : 0) + nb * F + (t >> 1)];
   i32x16 acc[S::RT][S::CT];
 #pragma unroll
   for (int i = 0; i < S::RT; i++)
@@ -207,11 +220,13 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
     for (int j = 0; j < S::CT; j++)
 #pragma unroll
       for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
-  constexpr int SB = large_stage_bytes<NPOS>();
-  static_assert(NPOS <= BM && large_bufs<NPOS>() * SB <= (int)sizeof(L.buf), "stage buffers");
-  large_loop<NPOS, large_bufs<NPOS>(), S::WR, S::WC, S::RT, S::CT>(ap, bp, H / kLargeK, L.buf, L.buf + SB,
-                                                        L.buf + 2 * SB, acc);
+  static_assert(NPOS <= BM && S::NBUF * S::STAGE <= (int)sizeof(L.buf), "stage buffers");
+  large_loop<ROWS, NPOS, S::NBUF, S::WR, S::WC, S::RT, S::CT>(
+      ap, tokens, H / kLargeK, L.buf, L.buf + S::STAGE, L.buf + 2 * S::STAGE, acc);
   const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
+  if (t < ROWS) L.ws[t] = ws_t;
+  if (t < NPOS) L.as[t] = as_t;
+  __syncthreads();
   float sx[S::CT];
 #pragma unroll
   for (int j = 0; j < S::CT; j++) sx[j] = L.as[(wc * S::CT + j) * 32 + r32];
@@ -232,36 +247,40 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
           hv[u] = g * __builtin_amdgcn_rcpf(1.0f + e) * up;
         }
         const int p = (wc * S::CT + j) * 32 + r32;
-        *reinterpret_cast<uint32_t*>(L.buf + p * 256 + (((r >> 4) ^ (p & 15)) << 4) +
+        *reinterpret_cast<uint32_t*>(L.buf + p * (2 * F) + (((r >> 4) ^ (p & (F / 8 - 1))) << 4) +
                                      (r & 15)) = pack_bf16(hv[0], hv[1]);
       }
     }
   __syncthreads();
-  store_rows<16>(L.buf, tl.mt, reinterpret_cast<char*>(h + (size_t)tl.p0 * I + nb * 128),
+  store_rows<F / 8>(L.buf, tl.mt, reinterpret_cast<char*>(h + (size_t)tl.p0 * I + nb * F),
                  (size_t)I * 2);
 }
 
-template <int NPOS, int BM, bool YB>
+template <int ROWS, int NPOS, int BM, bool YB>
 __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, const float* w2_scale,
                                               const Tile& tl, int nb, int H, int I,
-                                              const float* hs, void* y, LargeLds<BM>& L) {
-  typedef LargeShape<NPOS> S;
+                                              const float* hs, void* y, LargeLds<ROWS, BM>& L) {
+  typedef LargeShape<ROWS, NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
-  const char* ap[8];
+  constexpr int NA = ROWS / 32;
+  const char* ap[NA];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const int r = (w * 8 + i) * 8 + (lane >> 3);
-    const int row = min(nb * kLargeRows + r, H - 1);
+  for (int i = 0; i < NA; i++) {
+    const int r = (w * NA + i) * 8 + (lane >> 3);
+    const int row = min(nb * ROWS + r, H - 1);
     ap[i] = w2 + ((size_t)tl.e * H + row) * I + (((lane & 7) ^ swz_l(r)) << 4);
   }
-  const char* bp[NPOS / 32];
+  auto tokens = [&](const char*(&bp)[NPOS / 32]) {
 #pragma unroll
-  for (int i = 0; i < NPOS / 32; i++) {
-    const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
-    bp[i] = b + (size_t)(tl.p0 + min(r, tl.mt - 1)) * I + (((lane & 7) ^ swz_l(r)) << 4);
-  }
-  L.ws[t] = w2_scale[(size_t)tl.e * H + min(nb * kLargeRows + t, H - 1)];
-  if (t < NPOS) L.as[t] = hs[tl.p0 + min(t, tl.mt - 1)];
+    for (int i = 0; i < NPOS / 32; i++) {
+      const int r = (w * (NPOS / 32) + i) * 8 + (lane >> 3);
+      bp[i] = b + (size_t)(tl.p0 + min(r, tl.mt - 1)) * I + (((lane & 7) ^ swz_l(r)) << 4);
+    }
+  };
+  float ws_t = 0.f;
+  if (t < ROWS) ws_t = w2_scale[(size_t)tl.e * H + min(nb * ROWS + t, H - 1)];
+  float as_t = 0.f;
+  if (t < NPOS) as_t = hs[tl.p0 + min(t, tl.mt - 1)];
   i32x16 acc[S::RT][S::CT];
 #pragma unroll
   for (int i = 0; i < S::RT; i++)
@@ -269,17 +288,20 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
     for (int j = 0; j < S::CT; j++)
 #pragma unroll
       for (int q = 0; q < 16; q++) acc[i][j][q] = 0;
-  constexpr int SB = large_stage_bytes<NPOS>();
-  static_assert(NPOS <= BM && large_bufs<NPOS>() * SB <= (int)sizeof(L.buf), "stage buffers");
-  large_loop<NPOS, large_bufs<NPOS>(), S::WR, S::WC, S::RT, S::CT>(ap, bp, I / kLargeK, L.buf, L.buf + SB,
-                                                        L.buf + 2 * SB, acc);
+  static_assert(NPOS <= BM && S::NBUF * S::STAGE <= (int)sizeof(L.buf), "stage buffers");
+  large_loop<ROWS, NPOS, S::NBUF, S::WR, S::WC, S::RT, S::CT>(
+      ap, tokens, I / kLargeK, L.buf, L.buf + S::STAGE, L.buf + 2 * S::STAGE, acc);
   const int wr = w / S::WC, wc = w % S::WC, r32 = lane & 31, hi = lane >> 5;
+  if (t < ROWS) L.ws[t] = ws_t;
+  if (t < NPOS) L.as[t] = as_t;
+  __syncthreads();
   float sh[S::CT];
 #pragma unroll
   for (int j = 0; j < S::CT; j++) sh[j] = L.as[(wc * S::CT + j) * 32 + r32];
-  // a position's row in LDS holds 512 bytes: 256 channels in bf16, or in two
-  // passes 128 in fp32 (half of each wave's row tiles)
-  constexpr int PASSES = YB ? 1 : 2, RP = S::RT / PASSES, ES = YB ? 2 : 4;
+  // a position's row in LDS holds at most 512 bytes: every channel, or 256
+  // fp32 channels in two passes (half of each wave's row tiles)
+  constexpr int ES = YB ? 2 : 4, PASSES = ROWS * ES > 512 ? 2 : 1, RP = S::RT / PASSES;
+  constexpr int ROWB = ROWS * ES / PASSES, CH = ROWB / 16;
 #pragma unroll
   for (int pass = 0; pass < PASSES; pass++) {
     if (pass) __syncthreads();
@@ -297,7 +319,7 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
           for (int u = 0; u < 4; u++)
             v[u] = (float)acc[pass * RP + i][j][4 * q + u] * (ws[u] * sh[j]);
           const int p = (wc * S::CT + j) * 32 + r32;
-          char* dst = L.buf + p * 512 + (((o >> 4) ^ (p & 31)) << 4) + (o & 15);
+          char* dst = L.buf + p * ROWB + (((o >> 4) ^ (p & (CH - 1))) << 4) + (o & 15);
           if (YB)
             *reinterpret_cast<uint2*>(dst) =
                 make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
@@ -308,26 +330,41 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
     __syncthreads();
     // segments of RP * 32 channels per wave row
     constexpr int SEG = RP * 32 * ES / 16;  // chunks
-    for (int i = t; i < tl.mt * 32; i += 256) {
-      const int p = i / 32, c = i % 32;
-      const int ch = nb * kLargeRows + (c / SEG * S::RT + pass * RP) * 32 + c % SEG * 16 / ES;
+    for (int i = t; i < tl.mt * CH; i += 256) {
+      const int p = i / CH, c = i % CH;
+      const int ch = nb * ROWS + (c / SEG * S::RT + pass * RP) * 32 + c % SEG * 16 / ES;
       if (ch < H)
         *reinterpret_cast<uint4*>(reinterpret_cast<char*>(y) +
                                   ((size_t)(tl.p0 + p) * H + ch) * ES) =
-            *reinterpret_cast<const uint4*>(L.buf + p * 512 + ((c ^ (p & 31)) << 4));
+            *reinterpret_cast<const uint4*>(L.buf + p * ROWB + ((c ^ (p & (CH - 1))) << 4));
     }
   }
 }
 
-// Block -> (tile, row block): XCD x = b % 8 takes the row blocks x, x + 8, ...
-// of a tile, then those of the next one, so that its L2 holds one tile's rows
-// and an eighth of the expert's weights.  (2, 4, 8 and 16 tiles side by side on
-// a row block ran 0.6, 1.6, 3.5 and 4% slower on 8 experts of 2048 pairs.)
-__device__ __forceinline__ bool large_work(int n_tiles, int n_blk, int* tile, int* nb) {
-  const int x = blockIdx.x % 8, s = blockIdx.x / 8, per = (n_blk + 7) / 8;
-  *tile = s / per;
-  *nb = (s - *tile * per) * 8 + x;
-  return *tile < n_tiles && *nb < n_blk;
+// Block -> (tile, row block).  In order of the list, row block by row block
+// (a tile's blocks are dealt over the XCDs, so that each L2 holds a share of
+// the expert's weights for the expert's next tile); the 64-position tiles, of
+// experts that mostly have one, are dealt to the XCDs in contiguous eighths
+// instead, which reads a tile's rows into one L2.  Measured, list order
+// against eighths: 4096 tokens on 256 experts 2.81 / 2.86 ms a layer, 8 experts
+// of 2048 pairs 1.89 / 2.32 ms, down projection of 32 pairs per expert 0.688 /
+// 0.667 ms.
+template <int BM>
+__device__ __forceinline__ bool large_work(const Tile* tiles, const int32_t* num_tiles, int n_blk,
+                                           Tile* tl, int* nb) {
+  if constexpr (BM == 64) {
+    const int n = *num_tiles, x = blockIdx.x % 8, s = blockIdx.x / 8;
+    const int tile = (int)((long)x * n / 8) + s / n_blk;
+    *nb = s % n_blk;
+    if (tile >= (int)((long)(x + 1) * n / 8)) return false;
+    *tl = tiles[tile];
+    return true;
+  } else {
+    const int tile = blockIdx.x / n_blk;  // below the list's capacity
+    *nb = blockIdx.x - tile * n_blk;
+    *tl = tiles[tile];  // beside the count, not after it
+    return tile < *num_tiles;
+  }
 }
 
 // The narrowest main loop that holds a tile of mt positions.
@@ -341,48 +378,61 @@ __device__ __forceinline__ void by_width(int mt, F&& run) {
   run(std::integral_constant<int, 32>{});
 }
 
+// BM = 64 (experts of few dozen pairs, bound by their weights' stream): 128
+// rows, so that two blocks fit a CU and one streams while the other starts or
+// ends; else 256 rows.
+template <int BM>
+constexpr int large_rows() {
+  return BM == 64 ? 128 : 256;
+}
+
 template <int BM>
 __global__ __launch_bounds__(256)
-__attribute__((amdgpu_waves_per_eu(1, 1))) void w13_large_i8(
+__attribute__((amdgpu_waves_per_eu(BM == 64 ? 2 : 1, BM == 64 ? 2 : 1))) void w13_large_i8(
     const char* __restrict__ b, const char* __restrict__ w13, const float* __restrict__ w13_scale,
     const int32_t* __restrict__ sorted_ids, const Tile* __restrict__ tiles,
     const int32_t* __restrict__ num_tiles, int H, int I, int k, const float* __restrict__ xs,
     uint16_t* __restrict__ h) {
-  __shared__ __attribute__((aligned(16))) LargeLds<BM> L;
-  int tile, nb;
-  if (!large_work(*num_tiles, I / 128, &tile, &nb)) return;
-  const Tile tl = tiles[tile];
+  constexpr int ROWS = large_rows<BM>();
+  __shared__ __attribute__((aligned(16))) LargeLds<ROWS, BM> L;
+  Tile tl;
+  int nb;
+  if (!large_work<BM>(tiles, num_tiles, 2 * I / ROWS, &tl, &nb)) return;
   by_width<BM>(tl.mt, [&](auto n) {
-    w13_large_tile<n.value, BM>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
+    w13_large_tile<ROWS, n.value, BM>(b, w13, w13_scale, sorted_ids, tl, nb, H, I, k, xs, h, L);
   });
 }
 
 template <int BM, bool YB>
 __global__ __launch_bounds__(256)
-__attribute__((amdgpu_waves_per_eu(1, 1))) void w2_large_i8(
+__attribute__((amdgpu_waves_per_eu(BM == 64 ? 2 : 1, BM == 64 ? 2 : 1))) void w2_large_i8(
     const char* __restrict__ b, const char* __restrict__ w2, const float* __restrict__ w2_scale,
     const Tile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int H, int I,
     const float* __restrict__ hs, void* __restrict__ y) {
-  __shared__ __attribute__((aligned(16))) LargeLds<BM> L;
-  int tile, nb;
-  if (!large_work(*num_tiles, (H + kLargeRows - 1) / kLargeRows, &tile, &nb)) return;
-  const Tile tl = tiles[tile];
+  constexpr int ROWS = large_rows<BM>();
+  __shared__ __attribute__((aligned(16))) LargeLds<ROWS, BM> L;
+  Tile tl;
+  int nb;
+  if (!large_work<BM>(tiles, num_tiles, (H + ROWS - 1) / ROWS, &tl, &nb)) return;
   by_width<BM>(tl.mt, [&](auto n) {
-    w2_large_tile<n.value, BM, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+    w2_large_tile<ROWS, n.value, BM, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
   });
 }
 
-static long large_grid(long max_tiles, long n_blk) { return max_tiles * ((n_blk + 7) / 8) * 8; }
+static long large_grid(int bm, long max_tiles, long channels) {
+  const int rows = bm == 64 ? large_rows<64>() : large_rows<256>();
+  return (bm == 64 ? (max_tiles + 7) / 8 * 8 : max_tiles) * ((channels + rows - 1) / rows);
+}
 
 hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const float* w13_scale,
                                const int32_t* sorted_ids, const Tile* tiles,
                                const int32_t* num_tiles, int max_tiles, int H, int I, int k,
                                const float* xs, void* h, hipEvent_t e0, hipEvent_t e1,
                                hipStream_t st) {
-  const auto kern = bm == 256 ? w13_large_i8<256> : bm == 128 ? w13_large_i8<128> : w13_large_i8<64>;
-  launch_on(kern, dim3(large_grid(max_tiles, I / 128)), dim3(256), st, e0, e1,
-            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w13), w13_scale,
-            sorted_ids, tiles, num_tiles, H, I, k, xs, reinterpret_cast<uint16_t*>(h));
+  launch_on(bm == 64 ? w13_large_i8<64> : w13_large_i8<256>, dim3(large_grid(bm, max_tiles, 2L * I)),
+            dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
+            reinterpret_cast<const char*>(w13), w13_scale, sorted_ids, tiles, num_tiles, H, I, k,
+            xs, reinterpret_cast<uint16_t*>(h));
   return hipGetLastError();
 }
 
@@ -390,12 +440,11 @@ hipError_t launch_w2_large_i8(int bm, const void* b, const void* w2, const float
                               const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
                               int I, const float* hs, void* y, bool y_bf16, hipEvent_t e0,
                               hipEvent_t e1, hipStream_t st) {
-  const dim3 grid(large_grid(max_tiles, (H + kLargeRows - 1) / kLargeRows));
-  const auto kern = bm == 256   ? (y_bf16 ? w2_large_i8<256, true> : w2_large_i8<256, false>)
-                    : bm == 128 ? (y_bf16 ? w2_large_i8<128, true> : w2_large_i8<128, false>)
-                                : (y_bf16 ? w2_large_i8<64, true> : w2_large_i8<64, false>);
-  launch_on(kern, grid, dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
-            reinterpret_cast<const char*>(w2), w2_scale, tiles, num_tiles, H, I, hs, y);
+  const auto kern = bm == 64 ? (y_bf16 ? w2_large_i8<64, true> : w2_large_i8<64, false>)
+                             : (y_bf16 ? w2_large_i8<256, true> : w2_large_i8<256, false>);
+  launch_on(kern, dim3(large_grid(bm, max_tiles, H)), dim3(256), st, e0, e1,
+            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w2), w2_scale, tiles,
+            num_tiles, H, I, hs, y);
   return hipGetLastError();
 }
 

@@ -82,7 +82,6 @@ struct TileMma;
 // FP8: one v_mfma_scale_f32_16x16x128_f8f6f4 over chunks 2g and 2g+1.
 template <>
 struct TileMma<MOE_FP8_E4M3> {
-  typedef f32x4 Acc;
   static __device__ __forceinline__ int chunk(int g, int h) { return 2 * g + h; }
   static __device__ __forceinline__ f32x4 mma(i32x8 a, i32x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 127, 0, 127);
@@ -93,7 +92,6 @@ struct TileMma<MOE_FP8_E4M3> {
 // over chunk 4+g.
 template <>
 struct TileMma<MOE_BF16> {
-  typedef f32x4 Acc;
   static __device__ __forceinline__ int chunk(int g, int h) { return 4 * h + g; }
   static __device__ __forceinline__ f32x4 mma(i32x8 a, i32x8 b, f32x4 c) {
     i32x4 a0 = {a[0], a[1], a[2], a[3]}, a1 = {a[4], a[5], a[6], a[7]};
@@ -102,19 +100,6 @@ struct TileMma<MOE_BF16> {
                                                 __builtin_bit_cast(bf16x8, b0), c, 0, 0, 0);
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a1),
                                                    __builtin_bit_cast(bf16x8, b1), c, 0, 0, 0);
-  }
-};
-
-// int8: two v_mfma_i32_16x16x64_i8, over chunk g, then chunk 4+g; exact sums.
-template <>
-struct TileMma<MOE_INT8> {
-  typedef i32x4 Acc;
-  static __device__ __forceinline__ int chunk(int g, int h) { return 4 * h + g; }
-  static __device__ __forceinline__ i32x4 mma(i32x8 a, i32x8 b, i32x4 c) {
-    c = __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{a[0], a[1], a[2], a[3]},
-                                              i32x4{b[0], b[1], b[2], b[3]}, c, 0, 0, 0);
-    return __builtin_amdgcn_mfma_i32_16x16x64_i8(i32x4{a[4], a[5], a[6], a[7]},
-                                                 i32x4{b[4], b[5], b[6], b[7]}, c, 0, 0, 0);
   }
 };
 
@@ -136,8 +121,7 @@ constexpr int stage_lds_bytes() {
 
 template <int MODE, int BM, int WN, int PD, int MTA>
 __device__ __forceinline__ void tile_mainloop(const char* const* a_rows, const char* const* b_rows,
-                                              int n_stages, char* lds,
-                                              typename TileMma<MODE>::Acc (*acc)[MTA]) {
+                                              int n_stages, char* lds, f32x4 (*acc)[MTA]) {
   static_assert(BM / 16 <= MTA && (BM % (32 * WN) == 0 || BM == 16 * WN), "tile shape");
   typedef TileMma<MODE> M;
   constexpr int ROWB = kStageB;  // LDS bytes per token row
@@ -280,7 +264,7 @@ __device__ __forceinline__ void tile_mainloop(const char* const* a_rows, const c
 template <int MODE, int BM, int WN, int PD>
 __device__ __forceinline__ void run_mainloop(int mt, const char* const* a_rows,
                                              const char* const* b_rows, int n_stages, char* lds,
-                                             typename TileMma<MODE>::Acc (*acc)[BM / 16]) {
+                                             f32x4 (*acc)[BM / 16]) {
   if constexpr (BM == 128) {
     if (mt <= BM / 4) {
       tile_mainloop<MODE, BM / 4, WN, PD, BM / 16>(a_rows, b_rows, n_stages, lds, acc);
@@ -340,11 +324,11 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w13_swiglu_tiles(
     const int tok = sorted_ids[tl.p0 + j] / k;
     b_rows[i] = b + (size_t)tok * row_bytes + c * 16;
   }
-  typename TileMma<MODE>::Acc acc[2][MT];
+  f32x4 acc[2][MT];
 #pragma unroll
   for (int i = 0; i < 2; i++)
 #pragma unroll
-    for (int j = 0; j < MT; j++) acc[i][j] = typename TileMma<MODE>::Acc{0, 0, 0, 0};
+    for (int j = 0; j < MT; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   run_mainloop<MODE, BM, WN, PD>(tl.mt, a_rows, b_rows, (int)(row_bytes / kStageB), lds, acc);
 
   float cs = 1.0f;
@@ -358,9 +342,6 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w13_swiglu_tiles(
     const int col = j * 16 + r16;
     if (col < tl.mt) {
       uint16_t* hrow = reinterpret_cast<uint16_t*>(h) + (size_t)(tl.p0 + col) * I;
-      float sx = 1.0f;
-      if (MODE == MOE_INT8)
-        sx = reinterpret_cast<const float*>(act_amax_bits)[sorted_ids[tl.p0 + col] / k];
 #pragma unroll
       for (int i = 0; i < 2; i++) {
         const int f = nb * 64 * WN + (2 * w + i) * 8 + 2 * g;
@@ -371,11 +352,6 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w13_swiglu_tiles(
           if (is_fp8(MODE)) {
             gv *= cs;
             uv *= cs;
-          }
-          if (MODE == MOE_INT8) {
-            const float* ws = w13_scale + (size_t)tl.e * 2 * I + f + q;
-            gv *= sx * ws[0];
-            uv *= sx * ws[I];
           }
           hv[q] = gv / (1.0f + expf(-gv)) * uv;
         }
@@ -395,7 +371,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w13_swiglu_tiles(
 }
 
 // -------------------------------------------------------------------- w2
-// YB: y is stored in bf16 (the FP8 and INT8 fused paths; the scaled fp32 accumulators
+// YB: y is stored in bf16 (the FP8 fused path; the scaled fp32 accumulators
 // rounded to nearest even), else in fp32.
 template <int MODE, int BM, int WN, bool YB, int PD = kPD>
 __global__ __launch_bounds__(256 * WN)
@@ -406,7 +382,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w2_tiles(const char* __restrict_
                                                 const int32_t* __restrict__ num_tiles, int H, int I,
                                                 const uint32_t* act_amax_bits,
                                                 void* __restrict__ y) {
-  constexpr int ES = MODE == MOE_BF16 ? 2 : 1;
+  constexpr int ES = MODE == MOE_FP8_E4M3 ? 1 : 2;
   constexpr int MT = BM / 16;
   __shared__ __attribute__((aligned(16))) char lds[kTokBufs * BM * kStageB + 4096 * 4 * WN];
   const int NBLK = H / (kTileN * WN);
@@ -440,11 +416,11 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w2_tiles(const char* __restrict_
     const int j = min(r0 + 32 * WN * i, tl.mt - 1);
     b_rows[i] = b + (size_t)(tl.p0 + j) * row_bytes + c * 16;
   }
-  typename TileMma<MODE>::Acc acc[2][MT];
+  f32x4 acc[2][MT];
 #pragma unroll
   for (int i = 0; i < 2; i++)
 #pragma unroll
-    for (int j = 0; j < MT; j++) acc[i][j] = typename TileMma<MODE>::Acc{0, 0, 0, 0};
+    for (int j = 0; j < MT; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   run_mainloop<MODE, BM, WN, PD>(tl.mt, a_rows, b_rows, (int)(row_bytes / kStageB), lds, acc);
 
   float cs = 1.0f;
@@ -459,14 +435,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void w2_tiles(const char* __restrict_
       const size_t yo = (size_t)(tl.p0 + col) * H + nb * kTileN * WN + w * 32;
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        f32x4 v = {(float)acc[i][j][0], (float)acc[i][j][1], (float)acc[i][j][2],
-                   (float)acc[i][j][3]};
+        f32x4 v = acc[i][j];
         if (MODE == MOE_FP8_E4M3) v *= cs;
-        if (MODE == MOE_INT8) {
-          const size_t m = (size_t)tl.e * H + nb * kTileN * WN + w * 32 + i * 16 + 4 * g;
-          v *= *reinterpret_cast<const f32x4*>(w2_scale + m) *
-               reinterpret_cast<const float*>(act_amax_bits)[tl.p0 + col];
-        }
         const size_t o = yo + i * 16 + 4 * g;
         if (YB) {
           const uint32_t lo = (uint32_t)f32_to_bf16(v[0]) | ((uint32_t)f32_to_bf16(v[1]) << 16);
@@ -543,10 +513,6 @@ hipError_t launch_w13_tiles(int mode, int bm, const void* b, const void* w13,
     MOE_W13_TILES(MOE_FP8_E4M3, 64);
   else if (mode == MOE_FP8_E4M3 && bm == 128)
     MOE_W13_TILES(MOE_FP8_E4M3, 128);
-  else if (mode == MOE_INT8 && bm == 64)
-    MOE_W13_TILES(MOE_INT8, 64);
-  else if (mode == MOE_INT8 && bm == 128)
-    MOE_W13_TILES(MOE_INT8, 128);
   else
     return hipErrorInvalidValue;
 #undef MOE_W13_TILES
@@ -563,10 +529,12 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
 #define MOE_W2_TILES(MODE_, BM_, YB_)                                                           \
   launch_tiles_w2_mode<MODE_, BM_, YB_>(max_tiles, bb, ww, w2_scale, tiles, num_tiles, H, I,    \
                                         act_amax_bits, y, e0, e1, st)
-  if (y_bf16 && mode != MOE_FP8_E4M3 && mode != MOE_INT8) return hipErrorInvalidValue;
   if (mode == MOE_INT8)
     return launch_w2_large_i8(bm, b, w2, w2_scale, tiles, num_tiles, max_tiles, H, I,
                               reinterpret_cast<const float*>(act_amax_bits), y, y_bf16, e0, e1, st);
+  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
+  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
+  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
   if (mode == MOE_BF16 && bm == 64)
     MOE_W2_TILES(MOE_BF16, 64, false);
   else if (mode == MOE_BF16 && bm == 128)
@@ -579,14 +547,6 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
     MOE_W2_TILES(MOE_FP8_E4M3, 64, true);
   else if (mode == MOE_FP8_E4M3 && bm == 128)
     MOE_W2_TILES(MOE_FP8_E4M3, 128, true);
-  else if (mode == MOE_INT8 && bm == 64 && !y_bf16)
-    MOE_W2_TILES(MOE_INT8, 64, false);
-  else if (mode == MOE_INT8 && bm == 128 && !y_bf16)
-    MOE_W2_TILES(MOE_INT8, 128, false);
-  else if (mode == MOE_INT8 && bm == 64)
-    MOE_W2_TILES(MOE_INT8, 64, true);
-  else if (mode == MOE_INT8 && bm == 128)
-    MOE_W2_TILES(MOE_INT8, 128, true);
   else
     return hipErrorInvalidValue;
 #undef MOE_W2_TILES

@@ -153,13 +153,95 @@ struct XWork {
   uint8_t* xq;        // e4m3 codes
 };
 
+// Int8 codes of bf16 rows (MOE_INT8 mode): a row of x per token or of h per
+// pair, in a launch of its own or as extra blocks of another one.
+struct RowQuant {
+  const uint16_t* src;  // [rows, 8 * n8] bf16, 16-byte aligned
+  long rows;            // 0: nothing to do
+  int n8;
+  int8_t* codes;        // [rows, 8 * n8]
+  float* scales;        // [rows]
+};
+
+// Codes of one row by a block of THREADS: rne(127 a / amax), scale amax / 127.
+// The quotient must not be rounded before the rounding to an integer (a =
+// amax/2 is a tie that fl32(127/amax) * a misses): with r + r_lo = 127 / amax
+// to about 48 bits, fma(a, r, a * r_lo) is the quotient rounded once, and a
+// quotient of an 8-bit by an 8-bit significand that is no tie itself lies at
+// least 2^-17 away from one, so the integer is the exact one.  A row whose
+// amax is below 2^-100 is scaled up by 2^64 first, since 127 / amax would
+// overflow.  The first THREADS * VPT vectors of 8 stay in registers between
+// the maximum and the codes, the others are read twice.
+__device__ __forceinline__ float bf16x8_amax(i32x4 v) {
+  float m = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+    const uint32_t u = (uint32_t)v[q];
+    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint2 bf16x8_to_i8x8(i32x4 v, float up, float r, float r_lo) {
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    int c[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const uint32_t u = (uint32_t)v[2 * h + i / 2];
+      const float a = up * __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+      c[i] = (int)rintf(fmaf(a, r, a * r_lo));
+    }
+    w[h] = (uint32_t)(c[0] & 0xff) | (uint32_t)(c[1] & 0xff) << 8 | (uint32_t)(c[2] & 0xff) << 16 |
+           (uint32_t)c[3] << 24;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+template <int THREADS, int VPT>
+__device__ __forceinline__ void quant_i8_row(const RowQuant& rq, long row) {
+  __shared__ float part[THREADS / kWave];
+  const int t = threadIdx.x;
+  const i32x4* s4 = reinterpret_cast<const i32x4*>(rq.src) + row * rq.n8;
+  uint2* d2 = reinterpret_cast<uint2*>(rq.codes) + row * rq.n8;
+  i32x4 v[VPT];
+  float m = 0.f;
+#pragma unroll
+  for (int u = 0; u < VPT; u++) {
+    const int i = t + u * THREADS;
+    v[u] = i < rq.n8 ? s4[i] : i32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int u = 0; u < VPT; u++) m = fmaxf(m, bf16x8_amax(v[u]));
+  for (int i = t + VPT * THREADS; i < rq.n8; i += THREADS) m = fmaxf(m, bf16x8_amax(s4[i]));
+  m = wave_max(m);
+  if (lane_id() == 0) part[t / kWave] = m;
+  __syncthreads();
+  m = part[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / kWave; w++) m = fmaxf(m, part[w]);
+  const float up = m < 0x1p-100f ? 0x1p64f : 1.0f, mu = m * up;
+  const float r = mu > 0.f ? 127.0f / mu : 0.f;
+  const float r_lo = mu > 0.f ? fmaf(-r, mu, 127.0f) / mu : 0.f;
+  if (t == 0) rq.scales[row] = m > 0.f ? m / 127.0f : 1.0f;
+#pragma unroll
+  for (int u = 0; u < VPT; u++) {
+    const int i = t + u * THREADS;
+    if (i < rq.n8) d2[i] = bf16x8_to_i8x8(v[u], up, r, r_lo);
+  }
+  for (int i = t + VPT * THREADS; i < rq.n8; i += THREADS)
+    d2[i] = bf16x8_to_i8x8(s4[i], up, r, r_lo);
+}
+
 // --------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error.  All work goes to `st`.
 // With xw, the gating launch also writes the partial maxima of |x| and the
-// grouping launch (align sort or chunk sort) encodes x.
+// grouping launch (align sort or chunk sort) encodes x.  With rq.rows > 0,
+// the gating, front and tile-list launches carry the int8 rows of rq.
 hipError_t launch_topk_gating(const float* logits, int T, int E, int k, int renorm, int32_t* ids,
                               float* w, uint32_t* zero_words, int n_zero, hipStream_t st,
-                              const XWork* xw = nullptr);
+                              const XWork* xw = nullptr, const RowQuant& rq = RowQuant{});
 hipError_t launch_align_sort(const int32_t* ids, int T, int k, int E, int32_t* counts,
                              int32_t* offsets, int32_t* sorted_ids, int32_t* inv_perm,
                              hipStream_t st, const XWork* xw = nullptr);
@@ -175,7 +257,8 @@ hipError_t launch_route_small(const float* logits, int T, int E, int k, int reno
                               float* w, int32_t* counts, int32_t* offsets, int32_t* sorted_ids,
                               int32_t* inv_perm, int bm, bool big, Tile* tiles, Ctrl* ctrl,
                               const uint16_t* x, int H, uint8_t* xq, const uint16_t* wg,
-                              float* logits_out, hipStream_t st);
+                              float* logits_out, hipStream_t st,
+                              const RowQuant& rq = RowQuant{});
 // Grouping of n pairs in chunks of kSortChunk plus the tile list of <= bm
 // positions (three launches).  Scratch: chunk_counts and base hold
 // ceil(n / kSortChunk) * E ints each, rank n ints.
@@ -187,7 +270,8 @@ hipError_t launch_chunk_sort(const int32_t* ids, int n, int E, int32_t* counts, 
                              int32_t* rank, hipStream_t st, const XWork* xw = nullptr,
                              Tile* tiles_spread = nullptr);
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int bm, Tile* tiles,
-                              int32_t* num_tiles, hipStream_t st);
+                              int32_t* num_tiles, hipStream_t st,
+                              const RowQuant& rq = RowQuant{});
 hipError_t launch_zero_words(uint32_t* p, int n, hipStream_t st);
 // Router GEMM logits[t][e] = x[t] . wg[e] (fp32 accumulation); `tiles` holds
 // ceil(T / kRouterBM) entries and *num_tiles is written (tiled path only).
@@ -198,9 +282,7 @@ hipError_t launch_router_logits(int mode, const void* x, const void* wg, int T, 
 hipError_t launch_amax_bf16(const uint16_t* src, long n, uint32_t* amax_bits, hipStream_t st);
 hipError_t launch_quant_e4m3(const uint16_t* src, long n, const uint32_t* amax_bits, uint8_t* dst,
                              hipStream_t st);
-// Per-row int8 codes and scales (amax / 127) of a bf16 matrix, n a multiple of 8.
-hipError_t launch_quant_i8_rows(const uint16_t* src, long rows, int n, int8_t* codes,
-                                float* scales, hipStream_t st);
+hipError_t launch_quant_i8_rows(const RowQuant& rq, hipStream_t st);
 hipError_t launch_write_scales(const Ctrl* ctrl, float* act_scales, hipStream_t st);
 // scales[0] = amax / 448 (or 1) from the amax bits in scales[1].
 hipError_t launch_finish_scale(float* scales, hipStream_t st);

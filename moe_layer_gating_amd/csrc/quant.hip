@@ -122,100 +122,24 @@ hipError_t launch_finish_scale(float* scales, hipStream_t st) {
   return hipGetLastError();
 }
 
-// --------------------------------------------------------------- int8 rows
-// A block per row: codes rne(127 a / amax(row)), scale amax / 127.  The
-// quotient must not be rounded before the rounding to an integer (a = amax/2
-// is a tie that fl32(127/amax) * a misses): with r + r_lo = 127 / amax to
-// about 48 bits, fma(a, r, a * r_lo) is the quotient rounded once, and a
-// quotient of an 8-bit by an 8-bit significand that is no tie itself lies at
-// least 2^-17 away from one, so the integer is the exact one.  A row whose
-// amax is below 2^-100 is scaled up by 2^64 first, since 127 / amax would
-// overflow.  Rows of up to 256 * 8 * VPT values stay in registers between
-// the maximum and the codes; longer ones (VPT = 0) are read twice.
-__device__ __forceinline__ uint2 bf16x8_to_i8x8(i32x4 v, float up, float r, float r_lo) {
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; h++) {
-    int c[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const uint32_t u = (uint32_t)v[2 * h + i / 2];
-      const float a = up * __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
-      c[i] = (int)rintf(fmaf(a, r, a * r_lo));
-    }
-    w[h] = (uint32_t)(c[0] & 0xff) | (uint32_t)(c[1] & 0xff) << 8 | (uint32_t)(c[2] & 0xff) << 16 |
-           (uint32_t)c[3] << 24;
-  }
-  return make_uint2(w[0], w[1]);
-}
-
-__device__ __forceinline__ float bf16x8_amax(i32x4 v) {
-  float m = 0.f;
-#pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const uint32_t u = (uint32_t)v[q];
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
-  }
-  return m;
-}
-
+// Int8 rows (quant_i8_row), a block of 256 threads each, the row held in
+// registers between its maximum and its codes up to 16384 values.
 template <int VPT>
-__global__ __launch_bounds__(256) void quant_i8_rows_kernel(const uint16_t* __restrict__ src,
-                                                            int n8, int8_t* __restrict__ codes,
-                                                            float* __restrict__ scales) {
-  __shared__ float part[4];
-  constexpr int R = VPT ? VPT : 1;
-  const long row = blockIdx.x;
-  const i32x4* s4 = reinterpret_cast<const i32x4*>(src) + row * n8;
-  uint2* d2 = reinterpret_cast<uint2*>(codes) + row * n8;
-  i32x4 v[R];
-  float m = 0.f;
-  if (VPT) {
-#pragma unroll
-    for (int u = 0; u < VPT; u++) {
-      const int i = threadIdx.x + u * 256;
-      v[u] = i < n8 ? s4[i] : i32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int u = 0; u < VPT; u++) m = fmaxf(m, bf16x8_amax(v[u]));
-  } else {
-    for (int i = threadIdx.x; i < n8; i += 256) m = fmaxf(m, bf16x8_amax(s4[i]));
-  }
-  m = wave_max(m);
-  if (lane_id() == 0) part[threadIdx.x / kWave] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-  const float up = m < 0x1p-100f ? 0x1p64f : 1.0f, mu = m * up;
-  const float r = mu > 0.f ? 127.0f / mu : 0.f;
-  const float r_lo = mu > 0.f ? fmaf(-r, mu, 127.0f) / mu : 0.f;
-  if (threadIdx.x == 0) scales[row] = m > 0.f ? m / 127.0f : 1.0f;
-  if (VPT) {
-#pragma unroll
-    for (int u = 0; u < VPT; u++) {
-      const int i = threadIdx.x + u * 256;
-      if (i < n8) d2[i] = bf16x8_to_i8x8(v[u], up, r, r_lo);
-    }
-  } else {
-    for (int i = threadIdx.x; i < n8; i += 256) d2[i] = bf16x8_to_i8x8(s4[i], up, r, r_lo);
-  }
+__global__ __launch_bounds__(256) void quant_i8_rows_kernel(RowQuant rq) {
+  quant_i8_row<256, VPT>(rq, blockIdx.x);
 }
 
-hipError_t launch_quant_i8_rows(const uint16_t* src, long rows, int n, int8_t* codes,
-                                float* scales, hipStream_t st) {
-  const int n8 = n / 8;
-  if (rows <= 0) return hipSuccess;
-#define MOE_QUANT_I8(VPT_)   quant_i8_rows_kernel<VPT_><<<(unsigned)rows, 256, 0, st>>>(src, n8, codes, scales)
-  if (n8 <= 256)
-    MOE_QUANT_I8(1);
-  else if (n8 <= 512)
-    MOE_QUANT_I8(2);
-  else if (n8 <= 1024)
-    MOE_QUANT_I8(4);
-  else if (n8 <= 2048)
-    MOE_QUANT_I8(8);
+hipError_t launch_quant_i8_rows(const RowQuant& rq, hipStream_t st) {
+  if (rq.rows <= 0) return hipSuccess;
+  const unsigned n = (unsigned)rq.rows;
+  if (rq.n8 <= 256)
+    quant_i8_rows_kernel<1><<<n, 256, 0, st>>>(rq);
+  else if (rq.n8 <= 512)
+    quant_i8_rows_kernel<2><<<n, 256, 0, st>>>(rq);
+  else if (rq.n8 <= 1024)
+    quant_i8_rows_kernel<4><<<n, 256, 0, st>>>(rq);
   else
-    MOE_QUANT_I8(0);
-#undef MOE_QUANT_I8
+    quant_i8_rows_kernel<8><<<n, 256, 0, st>>>(rq);
   return hipGetLastError();
 }
 

@@ -258,9 +258,13 @@ __global__ __launch_bounds__(256) void topk_gating_kernel(const float* __restric
                                                           int32_t* __restrict__ ids,
                                                           float* __restrict__ wts,
                                                           uint32_t* zero_words, int n_zero,
-                                                          int gate_blocks, XWork xw) {
+                                                          int gate_blocks, XWork xw, RowQuant rq) {
   __shared__ __attribute__((aligned(16))) float gscr[4][kGateScratch];
   if ((int)blockIdx.x >= gate_blocks) {  // block-uniform
+    if (rq.rows) {
+      quant_i8_row<256, 4>(rq, blockIdx.x - gate_blocks);
+      return;
+    }
     x_amax_part(xw, blockIdx.x - gate_blocks, kXParts);
     return;
   }
@@ -274,12 +278,13 @@ __global__ __launch_bounds__(256) void topk_gating_kernel(const float* __restric
 
 hipError_t launch_topk_gating(const float* logits, int T, int E, int k, int renorm, int32_t* ids,
                               float* w, uint32_t* zero_words, int n_zero, hipStream_t st,
-                              const XWork* xw) {
+                              const XWork* xw, const RowQuant& rq) {
   const int tokens_per_block = 4;
   int grid = (T + tokens_per_block - 1) / tokens_per_block;
   if (grid < 1) grid = 1;
-  topk_gating_kernel<<<grid + (xw ? kXParts : 0), 256, 0, st>>>(
-      logits, T, E, k, renorm, ids, w, zero_words, n_zero, grid, xw ? *xw : XWork{});
+  // at most one of xw and rq
+  topk_gating_kernel<<<grid + (xw ? kXParts : (int)rq.rows), 256, 0, st>>>(
+      logits, T, E, k, renorm, ids, w, zero_words, n_zero, grid, xw ? *xw : XWork{}, rq);
   return hipGetLastError();
 }
 
@@ -393,14 +398,18 @@ hipError_t launch_align_sort(const int32_t* ids, int T, int k, int E, int32_t* c
 }
 
 // -------------------------------------------------------------- tile list
-// One block of 256 threads.  Expert e with c = offsets[e+1]-offsets[e] pairs
+// One block of 256 threads (further blocks encode an int8 row each).  Expert e with c = offsets[e+1]-offsets[e] pairs
 // contributes ceil(c / bm) tiles of at most bm consecutive sorted positions;
 // tiles are listed expert by expert.  The tile count goes to *num_tiles.
 __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restrict__ offsets,
                                                           int E,
                                                           int bm, Tile* __restrict__ tiles,
-                                                          int32_t* num_tiles) {
+                                                          int32_t* num_tiles, RowQuant rq) {
   __shared__ int tmp[4];
+  if (blockIdx.x > 0) {
+    quant_i8_row<256, 4>(rq, blockIdx.x - 1L);
+    return;
+  }
   int local[4], s = 0;
 #pragma unroll
   for (int q = 0; q < 4; q++) {
@@ -431,8 +440,8 @@ __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restr
 }
 
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int bm, Tile* tiles,
-                              int32_t* num_tiles, hipStream_t st) {
-  build_tiles_kernel<<<1, 256, 0, st>>>(offsets, E, bm, tiles, num_tiles);
+                              int32_t* num_tiles, hipStream_t st, const RowQuant& rq) {
+  build_tiles_kernel<<<1 + (unsigned)rq.rows, 256, 0, st>>>(offsets, E, bm, tiles, num_tiles, rq);
   return hipGetLastError();
 }
 
@@ -591,7 +600,8 @@ __device__ __forceinline__ int block_exclusive_scan_1024(int v, int* tmp, int* t
 //      order inside each expert;
 //   5. FP8 (xq != nullptr): amax(x) and the e4m3 codes of x, done by a second
 //      block of the same launch, concurrently with steps 1-4 (they share no
-//      data), so the two parts cost the longer of them rather than the sum.
+//      data), so the two parts cost the longer of them rather than the sum;
+//      INT8 (rq): the row codes of x, by a block per token.
 // Every control word is written here: amax_x (block 1 in FP8 mode, else 0),
 // amax_h = 0 and the tile counts (the list goes to num_tiles_big when `big`,
 // the tiled GEMMs' list, else to num_tiles; the other count is 0).
@@ -600,7 +610,12 @@ __global__ __launch_bounds__(1024) void route_small_kernel(
     float* __restrict__ wts, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
     int32_t* __restrict__ sorted_ids, int32_t* __restrict__ inv_perm, int bm, int big,
     Tile* __restrict__ tiles, Ctrl* ctrl, const uint16_t* __restrict__ x, int H,
-    uint8_t* __restrict__ xq, const uint16_t* __restrict__ wg, float* __restrict__ logits_out) {
+    uint8_t* __restrict__ xq, const uint16_t* __restrict__ wg, float* __restrict__ logits_out,
+    RowQuant rq) {
+  if (rq.rows && blockIdx.x > 0) {  // INT8: a block per row of x
+    quant_i8_row<1024, 1>(rq, blockIdx.x - 1L);
+    return;
+  }
   constexpr int NW = 16;
   __shared__ __attribute__((aligned(16))) int s_ids[kRouteSmallMax];
   __shared__ __attribute__((aligned(16))) float lgs[kFusedRouterMaxTE];
@@ -761,13 +776,14 @@ hipError_t launch_route_small(const float* logits, int T, int E, int k, int reno
                               float* w, int32_t* counts, int32_t* offsets, int32_t* sorted_ids,
                               int32_t* inv_perm, int bm, bool big, Tile* tiles, Ctrl* ctrl,
                               const uint16_t* x, int H, uint8_t* xq, const uint16_t* wg,
-                              float* logits_out, hipStream_t st) {
+                              float* logits_out, hipStream_t st, const RowQuant& rq) {
   if ((long)T * k > kRouteSmallMax || E > 1024) return hipErrorInvalidValue;
   if (wg && ((long)T * E > kFusedRouterMaxTE || (long)E * H > kFusedRouterMaxEH || !x || H % 128))
     return hipErrorInvalidValue;
-  route_small_kernel<<<xq ? 2 : 1, 1024, 0, st>>>(logits, T, E, k, renorm, ids, w, counts,
+  // at most one of xq and rq
+  route_small_kernel<<<xq ? 2 : 1 + (int)rq.rows, 1024, 0, st>>>(logits, T, E, k, renorm, ids, w, counts,
                                                  offsets, sorted_ids, inv_perm, bm, big ? 1 : 0,
-                                                 tiles, ctrl, x, H, xq, wg, logits_out);
+                                                 tiles, ctrl, x, H, xq, wg, logits_out, rq);
   return hipGetLastError();
 }
 
