@@ -26,6 +26,10 @@ LIB_PATH = os.path.join(_HERE, "libmoe_gfx950.so")
 _lib = None
 
 
+_current_device = torch.cuda.current_device
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class MoeError(RuntimeError):
     pass
 
@@ -156,11 +160,11 @@ def _gpu(t, name):
 def _run(what, dev, *args):
     """Calls `what` on GPU `dev`'s current stream, with that GPU current."""
     f = getattr(_lib or lib(), what)
-    if dev == torch.cuda.current_device():
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev == _current_device():
+        rc = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+            rc = f(*args, _raw_stream(dev))
     if rc != 0:
         _check(rc, what)
 

@@ -150,17 +150,18 @@ AlignLayout align_layout_for(int T, int k, int E) {
 
 // Workspace of moe_balance_loss: the blocks' partial sums.
 struct LossLayout {
-  size_t probs, counts, tokens, total;
+  size_t probs, counts, tokens, ticket, total;
 };
 
 LossLayout loss_layout_for(int T, int E) {
   LossLayout L;
-  const size_t nb = balance_loss_blocks(T);
+  const size_t nb = balance_loss_blocks(T, E);
   L.probs = 0;
   const size_t sums = align_up(nb * align_up((size_t)E, 4) * 4, 256);
   L.counts = sums;
   L.tokens = 2 * sums;
-  L.total = L.tokens + align_up(nb * 4, 256);
+  L.ticket = L.tokens + align_up(nb * 4, 256);
+  L.total = L.ticket + align_up(sizeof(LossTicket), 256);
   return L;
 }
 
@@ -482,7 +483,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
   return hip_status(launch_balance_loss(
       logits, topk_ids, T > 0 ? token_mask : nullptr, T, E, k, coef, loss, expert_counts,
       expert_probs, token_count, at<float>(ws, L.probs), at<int32_t>(ws, L.counts),
-      at<int32_t>(ws, L.tokens), reinterpret_cast<hipStream_t>(stream)));
+      at<int32_t>(ws, L.tokens), at<LossTicket>(ws, L.ticket),
+      reinterpret_cast<hipStream_t>(stream)));
 }
 
 int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,

@@ -329,15 +329,20 @@ hipError_t launch_inv_rope_fp8(const uint16_t* x, const int32_t* positions, cons
                                int T, int n_heads, int head_dim, int rot_dim, int max_pos,
                                bool interleaved, uint8_t* codes, float* scales, hipStream_t st);
 // Load-balance loss and router gradients (router_loss.hip).  The loss's
-// scratch holds balance_loss_blocks(T) rows of E (rounded up to 4) floats and
-// of as many ints, and balance_loss_blocks(T) ints (unused when that is 1).  The gradient adds the
+// scratch holds balance_loss_blocks rows of E (rounded up to 4) floats and
+// of as many ints, balance_loss_blocks ints and a LossTicket (unused when that is 1).  The gradient adds the
 // gating term when ids (with weights and grad_weights) are given and the
 // balance term when grad_loss (with counts and token_count) is.
-int balance_loss_blocks(int T);
+struct LossTicket {
+  int done;         // finishing blocks that have ended; cleared by the launch before
+  int pad;
+  double share[8];  // their shares of the loss
+};
+int balance_loss_blocks(int T, int E);
 hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                                int E, int k, float coef, float* loss, int32_t* counts,
                                float* probs, int32_t* token_count, float* part_p, int32_t* part_c,
-                               int32_t* part_n, hipStream_t st);
+                               int32_t* part_n, LossTicket* ticket, hipStream_t st);
 hipError_t launch_router_grad(const float* logits, const int32_t* ids, const float* weights,
                               const float* grad_weights, const uint8_t* mask,
                               const int32_t* counts, const int32_t* token_count,

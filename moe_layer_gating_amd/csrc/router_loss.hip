@@ -15,39 +15,44 @@
 //   plain softmax: d logits[e] = [e = id_j] w_j g_j - p_te S.
 //
 // Both directions are one pass over [T,E] fp32 rows and bound by HBM for
-// large batches, by launch latency for small ones.  16 lanes hold a row
-// (four rows per wave), each NC runs of 4 values, so the row reductions stay
-// inside the 16-lane rows that DPP moves reach at full rate.  No sum depends
+// large batches, by launch latency for small ones.  L = 16 lanes hold a row of
+// up to 256 logits (four rows per wave), each lane NC runs of 4 values, so the
+// row reductions stay inside the 16-lane rows that DPP moves reach at full
+// rate; longer rows take 32 or 64 lanes rather than more registers per lane
+// (16 lanes of 64 values held one wave per SIMD: 1024 experts at 2.3 TB/s).  No sum depends
 // on scheduling: blocks write partial sums that one block adds in block
 // order, and the counts are integers.
 #include "moe_common.h"
 
 namespace moe {
 
-constexpr int kRowLanes = 16;  // lanes per logits row (k <= 16: a lane per slot too)
-// threads of a loss block: 64 rows at a time (32 for the widest rows, whose
-// per-wave sums would not fit in LDS)
-__host__ __device__ constexpr int loss_threads(int nc) { return nc > 8 ? 512 : 1024; }
+constexpr int kLossThreads = 1024;
 constexpr int kGradThreads = 256;
 
-// Sum / maximum over the 16 lanes of a DPP row; every lane gets it.
+// Sum / maximum over the L lanes of a logits row; every lane gets it.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
+template <int L>
 __device__ __forceinline__ float row_sum(float v) {
   v += dpp<0xB1>(v);   // quad_perm [1,0,3,2]
   v += dpp<0x4E>(v);   // quad_perm [2,3,0,1]
   v += dpp<0x141>(v);  // row_half_mirror
   v += dpp<0x140>(v);  // row_mirror
+  if (L >= 32) v += __shfl_xor(v, 16);
+  if (L >= 64) v += __shfl_xor(v, 32);
   return v;
 }
+template <int L>
 __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, dpp<0xB1>(v));
   v = fmaxf(v, dpp<0x4E>(v));
   v = fmaxf(v, dpp<0x141>(v));
   v = fmaxf(v, dpp<0x140>(v));
+  if (L >= 32) v = fmaxf(v, __shfl_xor(v, 16));
+  if (L >= 64) v = fmaxf(v, __shfl_xor(v, 32));
   return v;
 }
 
@@ -58,20 +63,20 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Value q = 4c + i of lane l is expert (c * 16 + l) * 4 + i when E is a
-// multiple of 4 (16-byte loads), else (4c + i) * 16 + l.
-template <bool VEC>
+// Value q = 4c + i of lane l is expert (c * L + l) * 4 + i when E is a
+// multiple of 4 (16-byte loads), else (4c + i) * L + l.
+template <int L, bool VEC>
 __device__ __forceinline__ int expert_of(int c, int i, int l) {
-  return VEC ? (c * kRowLanes + l) * 4 + i : (4 * c + i) * kRowLanes + l;
+  return VEC ? (c * L + l) * 4 + i : (4 * c + i) * L + l;
 }
 
-template <int NC, bool VEC>
+template <int L, int NC, bool VEC>
 __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int l,
                                          float (&v)[4 * NC], float fill) {
 #pragma unroll
   for (int c = 0; c < NC; c++) {
     if (VEC) {
-      const int e = expert_of<true>(c, 0, l);
+      const int e = expert_of<L, true>(c, 0, l);
       f32x4 r = {fill, fill, fill, fill};
       if (e < E) r = *reinterpret_cast<const f32x4*>(row + e);
 #pragma unroll
@@ -79,7 +84,7 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, i
     } else {
 #pragma unroll
       for (int i = 0; i < 4; i++) {
-        const int e = expert_of<false>(c, i, l);
+        const int e = expert_of<L, false>(c, i, l);
         v[4 * c + i] = e < E ? row[e] : fill;
       }
     }
@@ -101,7 +106,7 @@ __device__ __forceinline__ float exp_neg(float x) {
 
 // Softmax of a row in place; NaN reads as -inf (as the gating reads it), and
 // a row without a finite logit becomes all zero.
-template <int N>
+template <int L, int N>
 __device__ __forceinline__ void softmax_row(float (&v)[N]) {
   float m = -INFINITY;
 #pragma unroll
@@ -109,7 +114,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[N]) {
     v[q] = v[q] == v[q] ? v[q] : -INFINITY;
     m = fmaxf(m, v[q]);
   }
-  m = row_max(m);
+  m = row_max<L>(m);
   if (m == -INFINITY) m = 0.f;
   float s = 0.f;
 #pragma unroll
@@ -117,7 +122,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[N]) {
     v[q] = exp_neg(v[q] - m);
     s += v[q];
   }
-  s = row_sum(s);
+  s = row_sum<L>(s);
   const float inv = s > 0.f ? 1.0f / s : 0.f;
 #pragma unroll
   for (int q = 0; q < N; q++) v[q] *= inv;
@@ -127,13 +132,12 @@ __device__ __forceinline__ bool row_live(const uint8_t* mask, long r, long end) 
   return r < end && (!mask || mask[r]);
 }
 
-// Turns expert e's sums over all tokens (thread e < E holds them) into the
-// outputs; called by every thread of one block.  red: one double per wave.
-__device__ __forceinline__ void finish_loss(double sum_p, int sum_c, int n, int E, int k,
-                                            float coef, float* loss, int32_t* counts,
-                                            float* probs, int32_t* token_count, double* red) {
-  const int e = threadIdx.x;
-  const double inv_n = n > 0 ? 1.0 / n : 0.0, p = sum_p * inv_n;
+// Writes expert e's count and mean probability from its sums over all tokens;
+// returns the block's sum of count * probability (valid in thread 0).  Thread
+// i holds expert e (none where e >= E); red: one double per wave.
+__device__ __forceinline__ double finish_experts(double sum_p, int sum_c, int n, int e, int E,
+                                                 int32_t* counts, float* probs, double* red) {
+  const double p = n > 0 ? sum_p / n : 0.0;
   double part = 0.0;
   if (e < E) {
     counts[e] = sum_c;
@@ -142,33 +146,36 @@ __device__ __forceinline__ void finish_loss(double sum_p, int sum_c, int n, int 
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
-  if (lane_id() == 0) red[e / kWave] = part;
+  if (lane_id() == 0) red[threadIdx.x / kWave] = part;
   __syncthreads();
-  if (e == 0) {
-    double s = 0.0;
-    for (int w = 0; w < (E + kWave - 1) / kWave; w++) s += red[w];
-    *loss = (float)((double)coef * E * s * inv_n / k);
-    *token_count = n;
-  }
+  if (threadIdx.x == 0)
+    for (int w = 1; w < (int)blockDim.x / kWave; w++) part += red[w];
+  return part;
+}
+
+__device__ __forceinline__ void finish_loss(double sum_cp, int n, int E, int k, float coef,
+                                            float* loss, int32_t* token_count) {
+  *loss = n > 0 ? (float)((double)coef * E * sum_cp / ((double)n * k)) : 0.f;
+  *token_count = n;
 }
 
 // Block b sums the probabilities and counts of rows [b rows, (b + 1) rows)
 // into row b of part_p and part_c (e4 values each) and part_n[b]; a single
 // block writes the outputs itself.
-template <int NC, bool VEC>
-__global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
+template <int L, int NC, bool VEC>
+__global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
     const uint8_t* __restrict__ mask, int T, int E, int k, int rows, float coef,
     float* __restrict__ part_p, int32_t* __restrict__ part_c, int32_t* __restrict__ part_n,
-    float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ probs,
-    int32_t* __restrict__ token_count) {
-  constexpr int N = 4 * NC, THREADS = loss_threads(NC), NW = THREADS / kWave;
-  constexpr int E_MAX = N * kRowLanes, STEP = THREADS / kRowLanes;
+    LossTicket* __restrict__ ticket, float* __restrict__ loss, int32_t* __restrict__ counts,
+    float* __restrict__ probs, int32_t* __restrict__ token_count) {
+  constexpr int N = 4 * NC, THREADS = kLossThreads, NW = THREADS / kWave;
+  constexpr int E_MAX = N * L, STEP = THREADS / L;
   __shared__ float wsum[NW][E_MAX];
   __shared__ int hist[E_MAX];
   __shared__ double red[NW];
   __shared__ int n_live;
-  const int t = threadIdx.x, l = t % kRowLanes, w = t / kWave;
+  const int t = threadIdx.x, l = t % L, w = t / kWave;
   const long lo = (long)blockIdx.x * rows, hi = min((long)T, lo + rows);
   for (int e = t; e < E; e += THREADS) hist[e] = 0;
   if (t == 0) n_live = 0;
@@ -181,10 +188,10 @@ __global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
   for (int q = 0; q < N; q++) acc[q] = 0.f;
   const long f0 = lo * k + t;
   const int id0 = f0 < hi * k && (!mask || mask[f0 / k]) ? ids[f0] : -1;
-  long r = lo + t / kRowLanes;
+  long r = lo + t / L;
   int live = 0;
   bool on = row_live(mask, r, hi), on1 = row_live(mask, r + STEP, hi);
-  if (on) load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
+  if (on) load_row<L, NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
   __syncthreads();
   if ((unsigned)id0 < (unsigned)E) atomicAdd(&hist[id0], 1);
   for (long f = f0 + THREADS; f < hi * k; f += THREADS) {
@@ -193,9 +200,9 @@ __global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
   }
   auto round = [&](float(&cur)[N], float(&next)[N]) {
     const bool on2 = row_live(mask, r + 2 * STEP, hi);
-    if (on1) load_row<NC, VEC>(logits + (size_t)(r + STEP) * E, E, l, next, -INFINITY);
+    if (on1) load_row<L, NC, VEC>(logits + (size_t)(r + STEP) * E, E, l, next, -INFINITY);
     if (on) {
-      softmax_row(cur);
+      softmax_row<L>(cur);
 #pragma unroll
       for (int q = 0; q < N; q++) acc[q] += cur[q];
       live++;
@@ -209,17 +216,17 @@ __global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
     round(w2, v);  // past the last row: nothing is on
   }
   if (l == 0 && live) atomicAdd(&n_live, live);
-  // the wave's four rows, then the waves in order
+  // the wave's rows, then the waves in order
 #pragma unroll
   for (int q = 0; q < N; q++) {
-    acc[q] += __shfl_xor(acc[q], 16);
-    acc[q] += __shfl_xor(acc[q], 32);
+    if (L <= 16) acc[q] += __shfl_xor(acc[q], 16);
+    if (L <= 32) acc[q] += __shfl_xor(acc[q], 32);
   }
-  if (lane_id() < kRowLanes) {
+  if (lane_id() < L) {
 #pragma unroll
     for (int c = 0; c < NC; c++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) wsum[w][expert_of<VEC>(c, i, l)] = acc[4 * c + i];
+      for (int i = 0; i < 4; i++) wsum[w][expert_of<L, VEC>(c, i, l)] = acc[4 * c + i];
   }
   __syncthreads();
   const int e4 = (E + 3) & ~3;
@@ -229,64 +236,49 @@ __global__ __launch_bounds__(loss_threads(NC)) void balance_loss_kernel(
 #pragma unroll
     for (int q = 0; q < NW; q++) s += wsum[q][e];
     if (single) {
-      wsum[0][e] = s;  // read by this thread alone until the barrier below
+      wsum[0][e] = s;  // this thread's expert
     } else {
       part_p[(size_t)blockIdx.x * e4 + e] = s;
       part_c[(size_t)blockIdx.x * e4 + e] = e < E ? hist[e] : 0;
     }
   }
   if (!single) {
-    if (t == 0) part_n[blockIdx.x] = n_live;
+    if (t == 0) {
+      part_n[blockIdx.x] = n_live;
+      if (blockIdx.x == 0) ticket->done = 0;  // for the launch after this one
+    }
     return;
   }
-  __syncthreads();
-  if constexpr (E_MAX > THREADS) {  // more experts than threads: two each
-    const double inv_n = n_live > 0 ? 1.0 / n_live : 0.0;
-    double part = 0.0;
-    for (int e = t; e < E; e += THREADS) {
-      const double p = wsum[0][e] * inv_n;
-      counts[e] = hist[e];
-      probs[e] = (float)p;
-      part += hist[e] * p;
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
-    if (lane_id() == 0) red[w] = part;
-    __syncthreads();
-    if (t == 0) {
-      double s = 0.0;
-      for (int q = 0; q < NW; q++) s += red[q];
-      *loss = (float)((double)coef * E * s * inv_n / k);
-      *token_count = n_live;
-    }
-  } else {
-    finish_loss(t < E ? wsum[0][t] : 0.0, t < E ? hist[t] : 0, n_live, E, k, coef, loss, counts,
-                probs, token_count, red);
-  }
+  const double cp = finish_experts(t < E ? wsum[0][t] : 0.0, t < E ? hist[t] : 0, n_live, t, E,
+                                   counts, probs, red);
+  if (t == 0) finish_loss(cp, n_live, E, k, coef, loss, token_count);
 }
 
-// One block adds the partial sums of n_parts blocks: thread (s, q) those of
-// experts 4q .. 4q+3 from blocks s, s + S, ... in order (16-byte loads, S as
-// large as 1024 threads allow, so that a slice is a few loads in flight at
-// once), then the S slices in order.
+// Adds the partial sums of n_parts blocks, 128 experts a block: thread (s, q)
+// those of experts 4q .. 4q+3 from blocks s, s + 32, ... in order (16-byte
+// loads, a few in flight at once), then the 32 slices in order.  The last
+// block to end adds the blocks' shares of the loss, in block order.  (One block
+// for all experts read 1024 experts' 2 MB in 20 us.)
+constexpr int kFinishExperts = 128;
 __global__ __launch_bounds__(1024) void balance_finish_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-    const int32_t* __restrict__ part_n, int n_parts, int E, int quads, int k, float coef,
+    const int32_t* __restrict__ part_n, LossTicket* ticket, int n_parts, int E, int k, float coef,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ probs,
     int32_t* __restrict__ token_count) {
-  __shared__ __attribute__((aligned(16))) double sp[4096];
-  __shared__ __attribute__((aligned(16))) int sc[4096];
+  constexpr int S = 32;
+  __shared__ __attribute__((aligned(16))) double sp[S][kFinishExperts];
+  __shared__ __attribute__((aligned(16))) int sc[S][kFinishExperts];
   __shared__ double red[16];
   __shared__ int live[16];
-  const int t = threadIdx.x, q = t % quads, s = t / quads, S = 1024 / quads;
+  const int t = threadIdx.x, q = t % S, s = t / S, e0 = blockIdx.x * kFinishExperts;
   const int e4 = (E + 3) & ~3;
   int n = t < n_parts ? part_n[t] : 0;  // n_parts <= 1024
   double p[4] = {0, 0, 0, 0};
   int c[4] = {0, 0, 0, 0};
-  if (4 * q < E) {
+  if (e0 + 4 * q < E) {
 #pragma unroll 4
     for (int b = s; b < n_parts; b += S) {
-      const size_t o = (size_t)b * e4 + 4 * q;
+      const size_t o = (size_t)b * e4 + e0 + 4 * q;
       const f32x4 pv = *reinterpret_cast<const f32x4*>(part_p + o);
       const i32x4 cv = *reinterpret_cast<const i32x4*>(part_c + o);
 #pragma unroll
@@ -297,27 +289,38 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; i++) {  // expert 4q + i of slice s
-    sp[s * 4 * quads + 4 * q + i] = p[i];
-    sc[s * 4 * quads + 4 * q + i] = c[i];
+  for (int i = 0; i < 4; i++) {
+    sp[s][4 * q + i] = p[i];
+    sc[s][4 * q + i] = c[i];
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
   if (lane_id() == 0) live[t / kWave] = n;
   __syncthreads();
-  double tp = 0.0;
-  int tc = 0;
   n = 0;
 #pragma unroll
   for (int w = 0; w < 16; w++) n += live[w];
-  if (t < E) {
-#pragma unroll 4
+  double tp = 0.0;
+  int tc = 0;
+  if (t < kFinishExperts) {
+#pragma unroll 8
     for (int x = 0; x < S; x++) {
-      tp += sp[x * 4 * quads + t];
-      tc += sc[x * 4 * quads + t];
+      tp += sp[x][t];
+      tc += sc[x][t];
     }
   }
-  finish_loss(tp, tc, n, E, k, coef, loss, counts, probs, token_count, red);
+  double cp = finish_experts(tp, tc, n, t < kFinishExperts ? e0 + t : E, E, counts, probs, red);
+  if (t > 0) return;
+  if (gridDim.x > 1) {
+    ticket->share[blockIdx.x] = cp;
+    __threadfence();
+    if (atomicAdd(&ticket->done, 1) != (int)gridDim.x - 1) return;
+    __threadfence();
+    cp = 0.0;
+    for (int b = 0; b < (int)gridDim.x; b++)
+      cp += __hip_atomic_load(&ticket->share[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  finish_loss(cp, n, E, k, coef, loss, token_count);
 }
 
 // Gradient rows.  SOFT: the row's softmax is needed (the balance term, or the
@@ -326,22 +329,22 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(
 // A selected expert's term reaches the lane that owns the expert through the
 // row's LDS copy: the lane of slot j adds the terms of every slot naming the
 // same expert in slot order, and the first of those slots writes the sum.
-template <int NC, bool VEC, bool SOFT, bool GATE>
+template <int L, int NC, bool VEC, bool SOFT, bool GATE>
 __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
     const float* __restrict__ weights, const float* __restrict__ grad_weights,
     const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts,
     const int32_t* __restrict__ token_count, const float* __restrict__ grad_loss, float coef,
     int renorm, int T, int E, int k, float* __restrict__ grad) {
-  constexpr int N = 4 * NC, E_MAX = N * kRowLanes, ROWS = kGradThreads / kRowLanes;
+  constexpr int N = 4 * NC, E_MAX = N * L, ROWS = kGradThreads / L, PER_WAVE = kWave / L;
   __shared__ __attribute__((aligned(16))) float sel[GATE ? ROWS : 1][GATE ? E_MAX : 4];
-  const int t = threadIdx.x, l = t % kRowLanes, g = t / kRowLanes;
+  const int t = threadIdx.x, l = t % L, g = t / L;
   const long step = (long)gridDim.x * ROWS;
   long r = (long)blockIdx.x * ROWS + g;
   // the first row is on its way while the counts are turned into d
   float v[N], v2[N];
   bool on = row_live(mask, r, T);
-  if (SOFT && on) load_row<NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
+  if (SOFT && on) load_row<L, NC, VEC>(logits + (size_t)r * E, E, l, v, -INFINITY);
   float d[N];
   float scale = 0.f;
   if (SOFT && grad_loss) {
@@ -352,12 +355,12 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     for (int c = 0; c < NC; c++) {
       i32x4 cv = {0, 0, 0, 0};
       if (VEC) {
-        const int e = expert_of<true>(c, 0, l);
+        const int e = expert_of<L, true>(c, 0, l);
         if (e < E) cv = *reinterpret_cast<const i32x4*>(counts + e);
       } else {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          const int e = expert_of<false>(c, i, l);
+          const int e = expert_of<L, false>(c, i, l);
           if (e < E) cv[i] = counts[e];
         }
       }
@@ -370,14 +373,14 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
   }
   if (GATE) {
 #pragma unroll
-    for (int q = 0; q < N; q++) sel[g][q * kRowLanes + l] = 0.f;
+    for (int q = 0; q < N; q++) sel[g][q * L + l] = 0.f;
     wave_lds_fence();
   }
-  // a wave's four rows take the same number of rounds: the LDS copy needs
+  // a wave's rows take the same number of rounds: the LDS copy needs
   // fences inside the wave only
   auto round = [&](float(&v)[N], float(&next)[N]) {
     const bool on1 = row_live(mask, r + step, T);
-    if (SOFT && on1) load_row<NC, VEC>(logits + (size_t)(r + step) * E, E, l, next, -INFINITY);
+    if (SOFT && on1) load_row<L, NC, VEC>(logits + (size_t)(r + step) * E, E, l, next, -INFINITY);
     float S = 0.f;
     int id = -1;
     if (GATE) {
@@ -394,13 +397,13 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
           wj = wg = 0.f;
         }
       }
-      S = row_sum(wg);
+      S = row_sum<L>(wg);
       const float term = renorm ? wg - wj * S : wg;
       float sum = 0.f;
       bool first = id >= 0;
       for (int j = 0; j < k; j++) {
-        const int idj = __shfl(id, j, kRowLanes);
-        const float tj = __shfl(term, j, kRowLanes);
+        const int idj = __shfl(id, j, L);
+        const float tj = __shfl(term, j, L);
         if (idj == id) {
           sum += tj;
           if (j < l) first = false;
@@ -411,11 +414,11 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     }
     if (on) {
       if (SOFT) {
-        softmax_row(v);
+        softmax_row<L>(v);
         float dp = 0.f;
 #pragma unroll
         for (int q = 0; q < N; q++) dp = fmaf(d[q], v[q], dp);
-        dp = row_sum(dp);
+        dp = row_sum<L>(dp);
         const float s0 = GATE && !renorm ? S : 0.f;
 #pragma unroll
         for (int q = 0; q < N; q++) v[q] *= scale * (d[q] - dp) - s0;
@@ -424,13 +427,13 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
 #pragma unroll
         for (int c = 0; c < NC; c++) {
           if (VEC) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(&sel[g][expert_of<true>(c, 0, l)]);
+            const f32x4 a = *reinterpret_cast<const f32x4*>(&sel[g][expert_of<L, true>(c, 0, l)]);
 #pragma unroll
             for (int i = 0; i < 4; i++) v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + a[i];
           } else {
 #pragma unroll
             for (int i = 0; i < 4; i++)
-              v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + sel[g][expert_of<false>(c, i, l)];
+              v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + sel[g][expert_of<L, false>(c, i, l)];
           }
         }
       }
@@ -443,14 +446,14 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
 #pragma unroll
       for (int c = 0; c < NC; c++) {
         if (VEC) {
-          const int e = expert_of<true>(c, 0, l);
+          const int e = expert_of<L, true>(c, 0, l);
           if (e < E)
             *reinterpret_cast<f32x4*>(out + e) =
                 f32x4{v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]};
         } else {
 #pragma unroll
           for (int i = 0; i < 4; i++) {
-            const int e = expert_of<false>(c, i, l);
+            const int e = expert_of<L, false>(c, i, l);
             if (e < E) out[e] = v[4 * c + i];
           }
         }
@@ -464,53 +467,53 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     on = on1;
     r += step;
   };
-  while (r - (g & 3) < T) {  // the next row is on its way while one is worked on
+  while (r - g % PER_WAVE < T) {  // the next row is on its way while one is worked on
     round(v, v2);
     round(v2, v);  // past the last row: nothing is read or written
   }
 }
 
-// Blocks of the loss kernel: at least 64 rows each (the finishing block reads
-// E sums per block), at most one per CU.
-int balance_loss_blocks(int T) {
-  const int b = (T + 63) / 64;
-  return T <= 128 ? 1 : (b > 256 ? 256 : b);
+inline int row_lanes(int E) { return E <= 256 ? 16 : E <= 512 ? 32 : 64; }
+
+// Blocks of the loss kernel: as many rows as a block takes at once, at most
+// one block per CU; one block up to twice that many rows, which saves the
+// finishing launch.
+int balance_loss_blocks(int T, int E) {
+  const int rows = kLossThreads / row_lanes(E), b = (T + rows - 1) / rows;
+  return b <= 2 ? 1 : (b > 256 ? 256 : b);
 }
 
-#define MOE_BY_EXPERTS(CALL)                                              \
-  do {                                                                    \
-    if (E % 4 == 0) {                                                     \
-      if (E <= 64) CALL(1, true);                                         \
-      else if (E <= 128) CALL(2, true);                                   \
-      else if (E <= 256) CALL(4, true);                                   \
-      else if (E <= 512) CALL(8, true);                                   \
-      else CALL(16, true);                                                \
-    } else {                                                              \
-      if (E <= 64) CALL(1, false);                                        \
-      else if (E <= 128) CALL(2, false);                                  \
-      else if (E <= 256) CALL(4, false);                                  \
-      else if (E <= 512) CALL(8, false);                                  \
-      else CALL(16, false);                                               \
-    }                                                                     \
+#define MOE_BY_EXPERTS_AS(CALL, VEC_)    \
+  do {                                   \
+    if (E <= 64) CALL(16, 1, VEC_);      \
+    else if (E <= 128) CALL(16, 2, VEC_); \
+    else if (E <= 256) CALL(16, 4, VEC_); \
+    else if (E <= 512) CALL(32, 4, VEC_); \
+    else CALL(64, 4, VEC_);              \
+  } while (0)
+#define MOE_BY_EXPERTS(CALL)            \
+  do {                                  \
+    if (E % 4 == 0)                     \
+      MOE_BY_EXPERTS_AS(CALL, true);    \
+    else                                \
+      MOE_BY_EXPERTS_AS(CALL, false);   \
   } while (0)
 
 hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                                int E, int k, float coef, float* loss, int32_t* counts,
                                float* probs, int32_t* token_count, float* part_p, int32_t* part_c,
-                               int32_t* part_n, hipStream_t st) {
-  const int nb = balance_loss_blocks(T), rows = (T + nb - 1) / nb;
-#define MOE_LOSS(NC_, VEC_)                                                                    \
-  balance_loss_kernel<NC_, VEC_><<<nb, loss_threads(NC_), 0, st>>>(                                 \
-      logits, ids, mask, T, E, k, rows, coef, part_p, part_c, part_n, loss, counts, probs,     \
-      token_count)
+                               int32_t* part_n, LossTicket* ticket, hipStream_t st) {
+  const int nb = balance_loss_blocks(T, E), rows = (T + nb - 1) / nb;
+#define MOE_LOSS(L_, NC_, VEC_)                                                                \
+  balance_loss_kernel<L_, NC_, VEC_><<<nb, kLossThreads, 0, st>>>(                             \
+      logits, ids, mask, T, E, k, rows, coef, part_p, part_c, part_n, ticket, loss, counts,    \
+      probs, token_count)
   MOE_BY_EXPERTS(MOE_LOSS);
 #undef MOE_LOSS
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || nb == 1) return err;
-  int quads = 1;
-  while (4 * quads < E) quads *= 2;
-  balance_finish_kernel<<<1, 1024, 0, st>>>(part_p, part_c, part_n, nb, E, quads, k, coef, loss,
-                                            counts, probs, token_count);
+  balance_finish_kernel<<<(E + kFinishExperts - 1) / kFinishExperts, 1024, 0, st>>>(
+      part_p, part_c, part_n, ticket, nb, E, k, coef, loss, counts, probs, token_count);
   return hipGetLastError();
 }
 
@@ -520,17 +523,18 @@ hipError_t launch_router_grad(const float* logits, const int32_t* ids, const flo
                               const float* grad_loss, float coef, int renorm, int T, int E, int k,
                               float* grad, hipStream_t st) {
   const bool gate = ids != nullptr, soft = grad_loss || !renorm;
-  long nb = ((long)T + kGradThreads / kRowLanes - 1) / (kGradThreads / kRowLanes);
+  const int rows = kGradThreads / row_lanes(E);  // of a block at a time
+  long nb = ((long)T + rows - 1) / rows;
   if (nb > 2048) nb = 2048;
-#define MOE_GRAD_AS(NC_, VEC_, SOFT_, GATE_)                                                    \
-  router_grad_kernel<NC_, VEC_, SOFT_, GATE_><<<(int)nb, kGradThreads, 0, st>>>(                \
+#define MOE_GRAD_AS(L_, NC_, VEC_, SOFT_, GATE_)                                                 \
+  router_grad_kernel<L_, NC_, VEC_, SOFT_, GATE_><<<(int)nb, kGradThreads, 0, st>>>(                \
       logits, ids, weights, grad_weights, mask, counts, token_count, grad_loss, coef, renorm, T, \
       E, k, grad)
-#define MOE_GRAD(NC_, VEC_)                          \
+#define MOE_GRAD(L_, NC_, VEC_)                      \
   do {                                               \
-    if (!gate) MOE_GRAD_AS(NC_, VEC_, true, false);  \
-    else if (soft) MOE_GRAD_AS(NC_, VEC_, true, true); \
-    else MOE_GRAD_AS(NC_, VEC_, false, true);        \
+    if (!gate) MOE_GRAD_AS(L_, NC_, VEC_, true, false);  \
+    else if (soft) MOE_GRAD_AS(L_, NC_, VEC_, true, true); \
+    else MOE_GRAD_AS(L_, NC_, VEC_, false, true);        \
   } while (0)
   MOE_BY_EXPERTS(MOE_GRAD);
 #undef MOE_GRAD

@@ -34,8 +34,9 @@ def _dev(a):
 
 
 def _rows_in_a_row(T):
-    blocks = 1 if T <= 128 else min(256, (T + 63) // 64)
-    return -(-(-(-T // blocks)) // 32)
+    # a block works on 16 to 64 rows at a time, and on more than twice that many
+    # only where 256 blocks are not enough
+    return max(2, -(-(-(-T // 256)) // 16))
 
 
 def _within(got, want, bound, what):
