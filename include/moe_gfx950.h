@@ -46,7 +46,9 @@
  *                  expert and output channel (w13_scale [E,2I], w2_scale
  *                  [E,H]); x and h are quantised to int8 inside the layer with
  *                  one dynamic scale per row (moe_act_quant_i8); the products
- *                  of codes are summed exactly in 32-bit integers.  H and I
+ *                  of codes are summed exactly in 32-bit integers.  With 16 or
+ *                  more pairs per expert on average the fused entry points
+ *                  round y to bf16 before the aggregation (as FP8 does).  H and I
  *                  are at most 131072 in this mode (MOE_ERR_UNSUPPORTED), so
  *                  that no such sum overflows.
  * Layouts (row-major, last index contiguous):
@@ -412,7 +414,8 @@ int moe_fused_forward_router(const moe_shape* s, const void* x, const void* wg, 
  * Boundaries 4-7 are the GEMM kernels' own start and end times (attached to
  * their dispatches, no marker packets around them), so 4->5 and 6->7 are
  * exactly those kernels' durations; 3->4 holds the FP8 x quantisation and
- * 5->6 the FP8 h quantisation.  The others are marker events on `stream`.
+ * 5->6 the FP8 or INT8 h quantisation (the INT8 codes of x are formed in
+ * 0->1, beside the gating).  The others are marker events on `stream`.
  * For few-token batches (few pairs per expert and T*k <= 256) one kernel
  * runs gating, grouping, the tile list and the x quantisation, so
  * boundaries 1 to 3 fall at the same point after it.

@@ -173,6 +173,7 @@ def _check_i8(x, x_name, width, w, w_name, scale, ids=()):
     """INT8 mode: operand types and the scale per output channel (a scale of
     another mode's shape would be read out of range)."""
     dev = _gpu(x, x_name)
+    _need(dev == _current_device(), "%s must live on the current GPU" % x_name)
     _need(w.dim() == 3 and w.shape[2] == width, "%s must be [E, channels, %d]" % (w_name, width))
     _arg(x, x_name, torch.bfloat16, (x.shape[0], width), dev)
     _arg(w, w_name, torch.int8, w.shape, dev)
@@ -209,6 +210,12 @@ def moe_check_shape(shape):
 
 def moe_workspace_bytes(shape):
     return lib().moe_workspace_bytes(ctypes.byref(shape))
+
+
+def _workspace_i8(ws, dev):
+    """INT8 mode: a caller's workspace is bytes on the tensors' GPU."""
+    if ws is not None:
+        _arg(ws, "ws", torch.uint8, ws.shape, dev)
 
 
 def workspace(shape, device=None):
@@ -290,6 +297,7 @@ def moe_grouped_gemm_w13_swiglu(x, w13, w13_scale, sorted_ids, expert_offsets, k
     if mode == MOE_INT8:
         _check_i8(x, "x", H, w13, "w13", w13_scale,
                   (("sorted_ids", sorted_ids, T * k), ("expert_offsets", expert_offsets, E + 1)))
+        _workspace_i8(ws, x.get_device())
         if h is not None:
             _arg(h, "h", torch.bfloat16, (T * k, I), x.get_device())
     ws = workspace(shape, x.device) if ws is None else ws
@@ -314,6 +322,7 @@ def moe_grouped_gemm_w2(h, w2, w2_scale, expert_offsets, act_scales, k, ws=None,
     if mode == MOE_INT8:
         _need(n_pairs == T * k, "h must hold a multiple of k rows")
         _check_i8(h, "h", I, w2, "w2", w2_scale, (("expert_offsets", expert_offsets, E + 1),))
+        _workspace_i8(ws, h.get_device())
         if y is not None:
             _arg(y, "y", torch.float32, (n_pairs, H), h.get_device())
     ws = workspace(shape, h.device) if ws is None else ws
@@ -493,6 +502,7 @@ def moe_fused_forward(x, logits, w13, w13_scale, w2, w2_scale, k, renormalize=Tr
     if mode == MOE_INT8:
         _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
                         topk_weights)
+        _workspace_i8(ws, x.get_device())
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:
@@ -568,6 +578,7 @@ def moe_fused_forward_router(x, wg, w13, w13_scale, w2, w2_scale, k, renormalize
     if mode == MOE_INT8:
         _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
                         topk_weights)
+        _workspace_i8(ws, x.get_device())
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:
@@ -592,6 +603,7 @@ def moe_fused_forward_events(x, logits, w13, w13_scale, w2, w2_scale, k, events,
     if mode == MOE_INT8:
         _check_i8_layer(x, w13, w13_scale, w2, w2_scale, T, H, E, I, k, out, logits, topk_ids,
                         topk_weights)
+        _workspace_i8(ws, x.get_device())
     shape = make_shape(T, H, E, k, I, mode, renormalize)
     ws = workspace(shape, x.device) if ws is None else ws
     if out is None:

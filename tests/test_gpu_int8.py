@@ -250,6 +250,34 @@ def test_router_noalloc_events_and_graph(T):
         assert torch.equal(buf, out)
 
 
+def test_two_layers_at_once():
+    """Two batches on two streams with a workspace each, enqueued alternately."""
+    H, E, k, I = 256, 12, 3, 384
+    sets = []
+    for T in (5, 700):
+        x, logits, w13, s13, w2, s2 = _layer(T, H, E, k, I, 0.5, T)
+        args = (x.cuda(), _dev(logits), _dev(w13), _dev(s13), _dev(w2), _dev(s2), k)
+        want = moe.moe_fused_forward(*args)
+        sets.append((args, want, torch.cuda.Stream(), torch.empty_like(want),
+                     moe.workspace(moe.make_shape(T, H, E, k, I, moe.MOE_INT8))))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for args, _, stream, out, ws in sets:
+            with torch.cuda.stream(stream):
+                moe.moe_fused_forward(*args, out=out, ws=ws)
+    torch.cuda.synchronize()
+    for _, want, _, out, _ in sets:
+        assert torch.equal(out, want)
+
+
+def test_other_modes_still_refuse_and_take_their_scales():
+    """float and FP8 weights keep their paths beside the INT8 one."""
+    with pytest.raises(moe.MoeError):
+        moe.mode_of(torch.zeros(1, dtype=torch.int16))
+    assert moe.mode_of(torch.zeros(1, dtype=torch.int8)) == moe.MOE_INT8
+    assert moe.mode_of(torch.zeros(1, dtype=torch.uint8)) == moe.MOE_FP8_E4M3
+
+
 def test_training_and_serving_steps_together():
     """One batch as a router's training step takes it: the int8 layer, the
     gradient of its gating weights (the derivative of <out, d> by w_tj is
@@ -294,6 +322,8 @@ def test_refusals_on_the_gpu():
                 (x, lg.double(), w13, s13, w2, s2), (x, lg, w13, s13, w2[:4], s2[:4])):
         with pytest.raises(moe.MoeError):
             moe.moe_fused_forward(*bad, 2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_fused_forward(x, lg, w13, s13, w2, s2, 2, ws=torch.empty(1 << 20, device="cuda"))
     with pytest.raises(moe.MoeError):
         moe.moe_act_quant_i8(x.float())
     with pytest.raises(moe.MoeError):
