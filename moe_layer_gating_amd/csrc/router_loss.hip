@@ -15,7 +15,10 @@
 //   plain softmax: d logits[e] = [e = id_j] w_j g_j - p_te S.
 //
 // Both directions are one pass over [T,E] fp32 rows and bound by HBM for
-// large batches, by launch latency for small ones.  L = 16 lanes hold a row of
+// large batches (131072 x 256: loss 33 us, its gradient 41 us, 4.1 and 6.5 TB/s
+// with the logits partly in the last-level cache; both gradients with plain
+// softmax 51 us), by launch latency for small ones (16 x 64: 3.3 and 2.2 us of
+// kernel under 7 us of host work per call).  L = 16 lanes hold a row of
 // up to 256 logits (four rows per wave), each lane NC runs of 4 values, so the
 // row reductions stay inside the 16-lane rows that DPP moves reach at full
 // rate; longer rows take 32 or 64 lanes rather than more registers per lane
