@@ -46,9 +46,10 @@
  *                  expert and output channel (w13_scale [E,2I], w2_scale
  *                  [E,H]); x and h are quantised to int8 inside the layer with
  *                  one dynamic scale per row (moe_act_quant_i8); the products
- *                  of codes are summed exactly in 32-bit integers.  With 16 or
- *                  more pairs per expert on average the fused entry points
- *                  round y to bf16 before the aggregation (as FP8 does).  H and I
+ *                  of codes are summed exactly in 32-bit integers.  Where y
+ *                  holds 2^24 values or more (T k H) and experts many pairs,
+ *                  the fused entry points round it to bf16 before the
+ *                  aggregation.  H and I
  *                  are at most 131072 in this mode (MOE_ERR_UNSUPPORTED), so
  *                  that no such sum overflows.
  * Layouts (row-major, last index contiguous):

@@ -79,28 +79,33 @@ def test_row_codes_of_no_rows_and_other_shapes():
 
 # ------------------------------------------------------------------ products
 # name, T, H, E, k, I, skew: one token, one expert, k = E; few and many pairs
-# per expert (16-, 64- and 128-position tiles), tiles that end ragged, experts
-# without a pair, row counts that are and are not multiples of 256 channels,
-# reductions of one to many 128-code stages, the three groupings
+# per expert, tiles that end ragged, experts without a pair, row counts that are
+# and are not multiples of 256 channels, reductions of one to many 128-code
+# stages, the three groupings
 LAYERS = [
+    # the few-token kernels (16-position tiles, several per expert in the last)
     ("one_token", 1, 512, 16, 4, 256, 0.0),
     ("one_expert", 5, 128, 1, 1, 128, 0.0),
     ("k_is_E", 6, 256, 4, 4, 128, 0.0),
     ("few_pairs", 16, 640, 16, 4, 384, 0.5),
     ("few_pairs_many_experts", 40, 256, 64, 8, 256, 0.5),
-    ("tiles_64", 100, 384, 10, 3, 640, 0.3),
-    ("tiles_64_skewed", 211, 256, 8, 2, 256, 2.0),
-    ("tiles_128", 600, 512, 8, 2, 512, 0.3),
-    ("tiles_128_skewed", 1037, 384, 12, 3, 384, 2.0),
-    ("tiles_128_odd_rows", 400, 128, 3, 1, 128, 0.5),
-    ("chunked", 1100, 256, 16, 8, 128, 1.0),
-    ("large_experts", 1500, 512, 2, 1, 768, 0.2),
-    # 256-position tiles (256 or more pairs per expert): odd and single stage
-    # counts, channels that are no multiple of 256, ragged, short and absent tiles
-    ("large_one_stage", 600, 128, 2, 1, 128, 0.5),
-    ("large_odd_stages", 1100, 384, 3, 2, 640, 1.0),
-    ("large_skewed", 2100, 256, 6, 2, 384, 2.5),
-    ("large_many_tiles", 4100, 256, 1, 1, 256, 0.0),
+    ("few_blocks", 100, 384, 10, 3, 640, 0.3),
+    ("few_blocks_skewed", 211, 256, 8, 2, 256, 2.0),
+    # 64-position tiles on 128 rows
+    ("small_tiles_9_pairs", 100, 256, 32, 3, 1024, 0.5),
+    ("small_tiles", 600, 512, 8, 2, 512, 0.3),
+    ("small_tiles_skewed", 1037, 384, 12, 3, 384, 2.0),
+    ("small_tiles_odd_rows", 400, 128, 3, 1, 128, 0.5),
+    ("small_tiles_chunked", 1100, 256, 16, 8, 128, 1.0),
+    ("small_tiles_one_stage", 600, 128, 2, 1, 128, 0.5),
+    ("small_tiles_odd_stages", 1100, 384, 3, 2, 640, 1.0),
+    ("small_tiles_one_expert", 4100, 256, 1, 1, 256, 0.0),
+    # 256-position tiles on 256 rows: every width of the main loop
+    ("large_tiles", 1100, 384, 8, 2, 2048, 0.7),
+    ("large_tiles_one_stage", 2100, 128, 4, 2, 2560, 0.5),
+    ("large_tiles_skewed", 1500, 256, 16, 2, 1920, 2.5),
+    ("large_tiles_one_expert", 5000, 256, 1, 1, 2048, 0.0),
+    ("large_tiles_prime", 1151, 640, 7, 3, 1664, 1.0),
 ]
 
 
@@ -155,12 +160,10 @@ def test_products_and_layer(c):
     want, bound = P.w2_i8(_np(h), w2, s2, offsets)
     _within(y.cpu().numpy(), want, bound, "y")
     assert torch.all(ybuf[T * k:] == 5.0)
-    # the fused call is the steps in one: the same h, and y rounded to bf16
-    # between its product and the aggregation when the tiled kernels run
+    # the fused call is the steps in one
     gids, gw = moe.moe_topk_gating(_dev(logits), k)
     assert np.array_equal(gids.cpu().numpy(), ids)
-    y_in = y.bfloat16().float() if T * k >= 16 * E else y
-    steps = moe.moe_combine(y_in, _dev(inv), gw, moe.MOE_INT8, E=E, I=I)
+    steps = moe.moe_combine(y, _dev(inv), gw, moe.MOE_INT8, E=E, I=I)
     out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
     ids_out = torch.empty(T, k, dtype=torch.int32, device="cuda")
     for _ in range(2):
@@ -169,14 +172,37 @@ def test_products_and_layer(c):
         assert np.array_equal(ids_out.cpu().numpy(), ids)
 
 
+@pytest.mark.parametrize("I", [128, 1024])  # 64- and 256-position tiles
+def test_layer_with_a_large_y(I):
+    """From 2^24 values on the fused call holds y in bf16: the steps' result
+    with their fp32 y rounded once, bit for bit."""
+    T, H, E, k = 4100, 2048, 5, 2
+    assert T * k * H >= 1 << 24
+    x, logits, w13, s13, w2, s2 = _layer(T, H, E, k, I, 0.3, 8)
+    ids, order, offsets, inv = _grouping(logits, k)
+    dx, d13, d2, ds13, ds2 = x.cuda(), _dev(w13), _dev(w2), _dev(s13), _dev(s2)
+    h, _ = moe.moe_grouped_gemm_w13_swiglu(dx, d13, ds13, _dev(order), _dev(offsets), k)
+    y = moe.moe_grouped_gemm_w2(h, d2, ds2, _dev(offsets), None, k)
+    rows = np.r_[0:40, 4000:4060, 8160:8200]  # of the first, a middle and the last expert
+    e = P.expert_of(offsets, T * k)[rows]
+    codes, s = P.quant_i8(_np(h)[rows])
+    want = np.stack([codes[i].astype(np.float64) @ w2[e[i]].astype(np.float64).T for i in range(rows.size)])
+    want *= s.astype(np.float64)[:, None] * s2.astype(np.float64)[e]
+    _within(y.cpu().numpy()[rows], want, np.abs(want) * 3.01 * P.U + 2.0 ** -140, "y")
+    gw = moe.moe_topk_gating(_dev(logits), k)[1]
+    steps = moe.moe_combine(y.bfloat16().float(), _dev(inv), gw, moe.MOE_INT8, E=E, I=I)
+    out = moe.moe_fused_forward(dx, _dev(logits), d13, ds13, d2, ds2, k)
+    assert torch.equal(out, steps)
+
+
 def test_longest_reduction_of_the_largest_codes():
     """131072 products of 127 and -128: sums of -2 130 706 432, the largest
-    that the mode lets occur, in both tile classes."""
+    that the mode lets occur, in the few-token kernel and both tile forms."""
     I, H = 131072, 128
     w2 = np.full((1, H, I), -128, np.int8)
     w2[0, 5] = 127
     s2 = np.full((1, H), 0.5, np.float32)
-    for n in (3, 40):
+    for n in (3, 40, 70):
         h = torch.full((n, I), 3.0, dtype=torch.bfloat16)
         h[1] = -0.75
         offsets = np.array([0, n], np.int32)
@@ -185,21 +211,24 @@ def test_longest_reduction_of_the_largest_codes():
         _within(y.cpu().numpy(), want, bound, "y")
 
 
-def test_weights_past_two_to_the_31_bytes():
-    """An expert whose codes start 2.1 GB into the tensor."""
+@pytest.mark.parametrize("n", [5, 600, 4300])
+def test_weights_past_two_to_the_31_bytes(n):
+    """An expert whose codes start 2.1 GB into the tensor (few-token kernel, 64-
+    and 256-position tiles)."""
     E, N, K = 66, 8192, 4096
     w2 = torch.zeros(E, N, K, dtype=torch.int8, device="cuda")
     g = torch.Generator(device="cuda").manual_seed(3)
     last = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
     w2[E - 1] = last
     s2 = torch.rand(E, N, generator=g, device="cuda")
-    h = torch.randn(5, K, generator=g, device="cuda").bfloat16()
+    h = torch.randn(n, K, generator=g, device="cuda").bfloat16()
     offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
-    offsets[E] = 5
+    offsets[E] = n
     y = moe.moe_grouped_gemm_w2(h, w2, s2, offsets, None, 1)
-    want, bound = P.w2_i8(_np(h), last.cpu().numpy()[None], s2[E - 1:].cpu().numpy(),
-                          np.array([0, 5]))
-    _within(y.cpu().numpy(), want, bound, "y")
+    rows = np.unique(np.array([0, 1, n // 2, n - 1]))
+    want, bound = P.w2_i8(_np(h)[rows], last.cpu().numpy()[None], s2[E - 1:].cpu().numpy(),
+                          np.array([0, rows.size]))
+    _within(y.cpu().numpy()[rows], want, bound, "y")
 
 
 @pytest.mark.parametrize("T", [4, 300])
