@@ -1,4 +1,4 @@
-// gemm_i8_large.hip -- grouped int8 expert products for 16 or more pairs per
+// gemm_i8_large.hip -- grouped int8 expert products for 8 or more pairs per
 // expert: acc[p][n] = sum_k q_a[p][k] q_w[e][n][k] in 32-bit integers (exact:
 // 128 * 127 * K < 2^31), scaled by fl32(s_a[p] * s_w[e][n]) in the epilogue.
 //

@@ -234,6 +234,22 @@ __device__ __forceinline__ void quant_i8_row(const RowQuant& rq, long row) {
     d2[i] = bf16x8_to_i8x8(s4[i], up, r, r_lo);
 }
 
+// Block b of row_quant_blocks(rq) takes rows b, b + blocks, ...: a row a block
+// up to 2^20 rows, so that a launch stays below 2^32 threads.
+constexpr long kRowQuantBlocks = 1L << 20;
+inline unsigned row_quant_blocks(const RowQuant& rq) {
+  return (unsigned)(rq.rows < kRowQuantBlocks ? rq.rows : kRowQuantBlocks);
+}
+
+template <int THREADS, int VPT>
+__device__ __forceinline__ void quant_i8_rows(const RowQuant& rq, long b) {
+  quant_i8_row<THREADS, VPT>(rq, b);
+  for (long row = b + kRowQuantBlocks; row < rq.rows; row += kRowQuantBlocks) {
+    __syncthreads();  // the row before is done with the LDS maxima
+    quant_i8_row<THREADS, VPT>(rq, row);
+  }
+}
+
 // --------------------------------------------------------------- launchers
 // Each returns hipSuccess or the launch error.  All work goes to `st`.
 // With xw, the gating launch also writes the partial maxima of |x| and the

@@ -122,16 +122,16 @@ hipError_t launch_finish_scale(float* scales, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Int8 rows (quant_i8_row), a block of 256 threads each, the row held in
+// Int8 rows (quant_i8_rows), a block of 256 threads each, the row held in
 // registers between its maximum and its codes up to 16384 values.
 template <int VPT>
 __global__ __launch_bounds__(256) void quant_i8_rows_kernel(RowQuant rq) {
-  quant_i8_row<256, VPT>(rq, blockIdx.x);
+  quant_i8_rows<256, VPT>(rq, blockIdx.x);
 }
 
 hipError_t launch_quant_i8_rows(const RowQuant& rq, hipStream_t st) {
   if (rq.rows <= 0) return hipSuccess;
-  const unsigned n = (unsigned)rq.rows;
+  const unsigned n = row_quant_blocks(rq);
   if (rq.n8 <= 256)
     quant_i8_rows_kernel<1><<<n, 256, 0, st>>>(rq);
   else if (rq.n8 <= 512)

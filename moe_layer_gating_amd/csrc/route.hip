@@ -262,7 +262,7 @@ __global__ __launch_bounds__(256) void topk_gating_kernel(const float* __restric
   __shared__ __attribute__((aligned(16))) float gscr[4][kGateScratch];
   if ((int)blockIdx.x >= gate_blocks) {  // block-uniform
     if (rq.rows) {
-      quant_i8_row<256, 4>(rq, blockIdx.x - gate_blocks);
+      quant_i8_rows<256, 4>(rq, blockIdx.x - gate_blocks);
       return;
     }
     x_amax_part(xw, blockIdx.x - gate_blocks, kXParts);
@@ -283,7 +283,7 @@ hipError_t launch_topk_gating(const float* logits, int T, int E, int k, int reno
   int grid = (T + tokens_per_block - 1) / tokens_per_block;
   if (grid < 1) grid = 1;
   // at most one of xw and rq
-  topk_gating_kernel<<<grid + (xw ? kXParts : (int)rq.rows), 256, 0, st>>>(
+  topk_gating_kernel<<<grid + (xw ? kXParts : (int)row_quant_blocks(rq)), 256, 0, st>>>(
       logits, T, E, k, renorm, ids, w, zero_words, n_zero, grid, xw ? *xw : XWork{}, rq);
   return hipGetLastError();
 }
@@ -398,8 +398,8 @@ hipError_t launch_align_sort(const int32_t* ids, int T, int k, int E, int32_t* c
 }
 
 // -------------------------------------------------------------- tile list
-// One block of 256 threads (further blocks encode an int8 row each).  Expert e with c = offsets[e+1]-offsets[e] pairs
-// contributes ceil(c / bm) tiles of at most bm consecutive sorted positions;
+// One block of 256 threads (further blocks encode int8 rows).  Expert e with
+// c = offsets[e+1]-offsets[e] pairs contributes ceil(c / bm) tiles of at most bm consecutive sorted positions;
 // tiles are listed expert by expert.  The tile count goes to *num_tiles.
 __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restrict__ offsets,
                                                           int E,
@@ -407,7 +407,7 @@ __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restr
                                                           int32_t* num_tiles, RowQuant rq) {
   __shared__ int tmp[4];
   if (blockIdx.x > 0) {
-    quant_i8_row<256, 4>(rq, blockIdx.x - 1L);
+    quant_i8_rows<256, 4>(rq, blockIdx.x - 1L);
     return;
   }
   int local[4], s = 0;
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restr
 
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int bm, Tile* tiles,
                               int32_t* num_tiles, hipStream_t st, const RowQuant& rq) {
-  build_tiles_kernel<<<1 + (unsigned)rq.rows, 256, 0, st>>>(offsets, E, bm, tiles, num_tiles, rq);
+  build_tiles_kernel<<<1 + row_quant_blocks(rq), 256, 0, st>>>(offsets, E, bm, tiles, num_tiles, rq);
   return hipGetLastError();
 }
 

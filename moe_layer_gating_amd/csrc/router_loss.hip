@@ -482,8 +482,8 @@ inline int row_lanes(int E) { return E <= 256 ? 16 : E <= 512 ? 32 : 64; }
 // one block per CU; one block up to twice that many rows, which saves the
 // finishing launch.
 int balance_loss_blocks(int T, int E) {
-  const int rows = kLossThreads / row_lanes(E), b = (T + rows - 1) / rows;
-  return b <= 2 ? 1 : (b > 256 ? 256 : b);
+  const long rows = kLossThreads / row_lanes(E), b = (T + rows - 1) / rows;
+  return b <= 2 ? 1 : (b > 256 ? 256 : (int)b);
 }
 
 #define MOE_BY_EXPERTS_AS(CALL, VEC_)    \
@@ -506,7 +506,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const ui
                                int E, int k, float coef, float* loss, int32_t* counts,
                                float* probs, int32_t* token_count, float* part_p, int32_t* part_c,
                                int32_t* part_n, LossTicket* ticket, hipStream_t st) {
-  const int nb = balance_loss_blocks(T, E), rows = (T + nb - 1) / nb;
+  const int nb = balance_loss_blocks(T, E), rows = (int)(((long)T + nb - 1) / nb);
 #define MOE_LOSS(L_, NC_, VEC_)                                                                \
   balance_loss_kernel<L_, NC_, VEC_><<<nb, kLossThreads, 0, st>>>(                             \
       logits, ids, mask, T, E, k, rows, coef, part_p, part_c, part_n, ticket, loss, counts,    \

@@ -67,6 +67,51 @@ def test_row_codes_over_the_whole_range():
     assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
 
 
+def test_row_codes_of_many_rows():
+    """2^24 + 5 rows, and the last of them: a block per row would be 2^32 threads."""
+    say("row codes of many rows")
+    rows, n = (1 << 24) + 5, 8
+    a = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")
+    a[:, 3] = 2
+    a[:, 5] = -1
+    a[1::7] *= 3
+    codes, scales = moe.moe_act_quant_i8(a)
+    want = torch.tensor([0, 0, 0, 127, 0, -64, 0, 0], dtype=torch.int8, device="cuda")
+    assert bool((codes == want).all())
+    amax = torch.full((rows,), 2.0, device="cuda")
+    amax[1::7] *= 3
+    # 2 and 6 over 127, rounded once
+    assert torch.equal(scales, torch.where(amax == 2, np.float32(2) / np.float32(127),
+                                           np.float32(6) / np.float32(127)))
+
+
+def test_layer_of_many_tokens():
+    """More tokens than row blocks (2^20) in the gating, the tile list and the
+    down projection; the first and last tokens against the same ones alone."""
+    say("layer of many tokens")
+    T, H, E, k, I = (1 << 20) + 700, 128, 2, 1, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    x[1 << 20:] *= 4
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    w13 = torch.randint(-127, 128, (E, 2 * I, H), generator=g, device="cuda").to(torch.int8)
+    w2 = torch.randint(-127, 128, (E, H, I), generator=g, device="cuda").to(torch.int8)
+    s13 = torch.rand(E, 2 * I, generator=g, device="cuda") * 1e-3
+    s2 = torch.rand(E, H, generator=g, device="cuda") * 1e-3
+    out = moe.moe_fused_forward(x, logits, w13, s13, w2, s2, k)
+    ids, wts = moe.moe_topk_gating(logits, k)
+    _, offsets, sorted_ids, inv = moe.moe_align_sort(ids, E)
+    h = moe.moe_grouped_gemm_w13_swiglu(x, w13, s13, sorted_ids, offsets, k)[0]
+    y = moe.moe_grouped_gemm_w2(h, w2, s2, offsets, None, k)
+    steps = moe.moe_combine(y, inv, wts, moe.MOE_INT8, E)
+    for part in (slice(0, 700), slice((1 << 20) - 350, (1 << 20) + 350), slice(T - 700, T)):
+        few = moe.moe_fused_forward(x[part].clone(), logits[part].clone(), w13, s13, w2, s2, k)
+        # exact: integer sums, one formula in both tile forms, one term (k = 1, weight 1),
+        # for which rounding y to bf16 first changes nothing
+        assert torch.equal(out[part], few)
+        assert torch.equal(steps[part], few)
+
+
 def test_row_codes_of_no_rows_and_other_shapes():
     codes, scales = moe.moe_act_quant_i8(torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"))
     assert codes.shape == (0, 64) and scales.shape == (0,)
