@@ -257,23 +257,26 @@ __global__ __launch_bounds__(kLossThreads) void balance_loss_kernel(
   if (t == 0) finish_loss(cp, n_live, E, k, coef, loss, token_count);
 }
 
-// Adds the partial sums of n_parts blocks, 128 experts a block: thread (s, q)
-// those of experts 4q .. 4q+3 from blocks s, s + 32, ... in order (16-byte
-// loads, a few in flight at once), then the 32 slices in order.  The last
-// block to end adds the blocks' shares of the loss, in block order.  (One block
-// for all experts read 1024 experts' 2 MB in 20 us.)
-constexpr int kFinishExperts = 128;
+// Adds the partial sums of n_parts blocks, FE experts a block: thread (s, q)
+// those of experts 4q .. 4q+3 from blocks s, s + S, ... in order (16-byte
+// loads, a few in flight at once), then the S slices in order.  With several
+// blocks the last one to end adds their shares of the loss, in block order.
+// One block for 256 experts' sums of up to 128 parts: the ticket's fence costs
+// 0.9 us of 5 (64 parts 5.0 -> 4.2 us; 256 parts 7.2 -> 9 us); beyond that 128
+// experts a block (one block for all read 1024 experts' 2 MB in 20 us).  Up to 64 experts
+// take twice the slices (256 parts of 61: 5.1 -> 4.7 us).
+template <int FE>
 __global__ __launch_bounds__(1024) void balance_finish_kernel(
     const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
     const int32_t* __restrict__ part_n, LossTicket* ticket, int n_parts, int E, int k, float coef,
     float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ probs,
     int32_t* __restrict__ token_count) {
-  constexpr int S = 32;
-  __shared__ __attribute__((aligned(16))) double sp[S][kFinishExperts];
-  __shared__ __attribute__((aligned(16))) int sc[S][kFinishExperts];
+  constexpr int Q = FE / 4, S = 1024 / Q;
+  __shared__ __attribute__((aligned(16))) double sp[S][FE];
+  __shared__ __attribute__((aligned(16))) int sc[S][FE];
   __shared__ double red[16];
   __shared__ int live[16];
-  const int t = threadIdx.x, q = t % S, s = t / S, e0 = blockIdx.x * kFinishExperts;
+  const int t = threadIdx.x, q = t % Q, s = t / Q, e0 = blockIdx.x * FE;
   const int e4 = (E + 3) & ~3;
   int n = t < n_parts ? part_n[t] : 0;  // n_parts <= 1024
   double p[4] = {0, 0, 0, 0};
@@ -305,14 +308,14 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(
   for (int w = 0; w < 16; w++) n += live[w];
   double tp = 0.0;
   int tc = 0;
-  if (t < kFinishExperts) {
+  if (t < FE) {
 #pragma unroll 8
     for (int x = 0; x < S; x++) {
       tp += sp[x][t];
       tc += sc[x][t];
     }
   }
-  double cp = finish_experts(tp, tc, n, t < kFinishExperts ? e0 + t : E, E, counts, probs, red);
+  double cp = finish_experts(tp, tc, n, t < FE ? e0 + t : E, E, counts, probs, red);
   if (t > 0) return;
   if (gridDim.x > 1) {
     ticket->share[blockIdx.x] = cp;
@@ -515,8 +518,16 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* ids, const ui
 #undef MOE_LOSS
   hipError_t err = hipGetLastError();
   if (err != hipSuccess || nb == 1) return err;
-  balance_finish_kernel<<<(E + kFinishExperts - 1) / kFinishExperts, 1024, 0, st>>>(
-      part_p, part_c, part_n, ticket, nb, E, k, coef, loss, counts, probs, token_count);
+#define MOE_FINISH(FE_, BLOCKS_)                                                              \
+  balance_finish_kernel<FE_><<<BLOCKS_, 1024, 0, st>>>(part_p, part_c, part_n, ticket, nb, E, \
+                                                       k, coef, loss, counts, probs, token_count)
+  if (E <= 64)
+    MOE_FINISH(64, 1);
+  else if (E > 128 && E <= 256 && nb <= 128)
+    MOE_FINISH(256, 1);
+  else
+    MOE_FINISH(128, (E + 127) / 128);
+#undef MOE_FINISH
   return hipGetLastError();
 }
 

@@ -16,7 +16,7 @@ pytestmark = pytest.mark.gpu
 # run in one block, 129 in several), rows that end inside a block
 SHAPES = [(1, 1, 1), (1, 64, 8), (3, 2, 2), (16, 8, 8), (33, 61, 6), (64, 64, 16), (127, 128, 2),
           (128, 260, 4), (129, 255, 3), (200, 256, 8), (512, 384, 5), (700, 1024, 16),
-          (1000, 1023, 7), (4099, 13, 4), (9001, 256, 8)]
+          (1000, 1023, 7), (600, 100, 4), (4099, 13, 4), (9001, 256, 8)]
 
 
 def _inputs(T, E, k, seed, masked, spread=2.0):
