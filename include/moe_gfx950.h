@@ -49,9 +49,8 @@
  *                  of codes are summed exactly in 32-bit integers.  Where y
  *                  holds 2^24 values or more (T k H) and experts many pairs,
  *                  the fused entry points round it to bf16 before the
- *                  aggregation.  H and I
- *                  are at most 131072 in this mode (MOE_ERR_UNSUPPORTED), so
- *                  that no such sum overflows.
+ *                  aggregation.  H and I are at most 131072 in this mode
+ *                  (MOE_ERR_UNSUPPORTED), so that no such sum overflows.
  * Layouts (row-major, last index contiguous):
  *   x [T,H]; logits [T,E] fp32; w13 [E,2I,H] (rows 0..I-1 gate, I..2I-1 up);
  *   w2 [E,H,I]; h [T*k,I] and y [T*k,H] in expert-sorted pair order;

@@ -24,8 +24,9 @@
 // matrix units at the clock the power limit leaves: without the epilogue 5%
 // less, without loads in the loop 22% less, with all loads from L2 9% less.
 // 4096 tokens on 256 experts (H 7168, I 2048): gate/up 1.63 ms, down 0.93 ms,
-// bound by the weights' stream (7.5 and 3.8 GB at 6.3 TB/s are 1.19 and 0.60
-// ms): without MFMAs 1.5% less, without token loads 8% less, without the output
+// bound by the memory system: 7.5 and 3.8 GB of weights (1.19 and 0.60 ms at
+// 6.3 TB/s) become 9.9 and 4.8 GB into the L2s, since each XCD reads a tile's
+// rows; without MFMAs 1.5% less, without token loads 8% less, without the output
 // 2% (gate/up) and 16% (down) less.  The register-ring tiles of gemm_tiles.hip,
 // given int8 operands, took 2.55, 1.88 and 1.11 ms for the three.
 #include <type_traits>
@@ -64,8 +65,8 @@ __device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0xc07f
 // gives those of the token loads, called once the first weights are on their
 // way (it may wait for the rows' token numbers).
 template <int ROWS, int NPOS, int NBUF, int WR, int WC, int RT, int CT, typename Tokens>
-__device__ __forceinline__ void large_loop(const char* (&ap)[ROWS / 32], Tokens&& tokens, int n_stages,
-                                           char* __restrict__ b0, char* __restrict__ b1,
+__device__ __forceinline__ void large_loop(const char* (&ap)[ROWS / 32], Tokens&& tokens,
+                                           int n_stages, char* __restrict__ b0, char* __restrict__ b1,
                                            char* __restrict__ b2, i32x16 (&acc)[RT][CT]) {
   static_assert(NBUF == 2 || NBUF == 3, "buffers");
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -186,9 +187,9 @@ struct LargeShape<256, 256> {
 
 // LDS: NBUF stage buffers of (ROWS + NPOS) rows of 128 bytes (the kernel's
 // widest tiles decide their size), then the block's channel and row scales.
-// The epilogue lays the output tile
-// over the stage buffers, a row of 16-byte chunks per position with chunk c
-// of row p at slot c ^ (p mod the row's chunks), and stores whole lines.
+// The epilogue lays the output tile over the stage buffers, a row of 16-byte
+// chunks per position with chunk c of row p at slot c ^ (p mod the row's
+// chunks), and stores whole lines.
 template <int ROWS, int BM>
 struct LargeLds {
   static constexpr int N = BM < 256 ? BM : 128;
@@ -216,7 +217,8 @@ template <int ROWS, int NPOS, int BM>
 __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
                                                const float* w13_scale, const int32_t* sorted_ids,
                                                const Tile& tl, int nb, int H, int I, int k,
-                                               const float* xs, uint16_t* h, LargeLds<ROWS, BM>& L) {
+                                               const float* xs, uint16_t* h,
+                                               LargeLds<ROWS, BM>& L) {
   typedef LargeShape<ROWS, NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
   constexpr int NA = ROWS / 32, F = ROWS / 2;  // weight loads of a lane, features
@@ -460,8 +462,8 @@ hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const flo
                                const int32_t* num_tiles, int max_tiles, int H, int I, int k,
                                const float* xs, void* h, hipEvent_t e0, hipEvent_t e1,
                                hipStream_t st) {
-  launch_on(bm == 64 ? w13_large_i8<64> : w13_large_i8<256>, dim3(large_grid(bm, max_tiles, 2L * I)),
-            dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
+  launch_on(bm == 64 ? w13_large_i8<64> : w13_large_i8<256>,
+            dim3(large_grid(bm, max_tiles, 2L * I)), dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
             reinterpret_cast<const char*>(w13), w13_scale, sorted_ids, tiles, num_tiles, H, I, k,
             xs, reinterpret_cast<uint16_t*>(h));
   return hipGetLastError();

@@ -346,9 +346,10 @@ hipError_t launch_inv_rope_fp8(const uint16_t* x, const int32_t* positions, cons
                                bool interleaved, uint8_t* codes, float* scales, hipStream_t st);
 // Load-balance loss and router gradients (router_loss.hip).  The loss's
 // scratch holds balance_loss_blocks rows of E (rounded up to 4) floats and
-// of as many ints, balance_loss_blocks ints and a LossTicket (unused when that is 1).  The gradient adds the
-// gating term when ids (with weights and grad_weights) are given and the
-// balance term when grad_loss (with counts and token_count) is.
+// of as many ints, balance_loss_blocks ints and a LossTicket (unused when that
+// is 1).  The gradient adds the gating term when ids (with weights and
+// grad_weights) are given and the balance term when grad_loss (with counts and
+// token_count) is.
 struct LossTicket {
   int done;         // finishing blocks that have ended; cleared by the launch before
   int pad;

@@ -399,8 +399,9 @@ hipError_t launch_align_sort(const int32_t* ids, int T, int k, int E, int32_t* c
 
 // -------------------------------------------------------------- tile list
 // One block of 256 threads (further blocks encode int8 rows).  Expert e with
-// c = offsets[e+1]-offsets[e] pairs contributes ceil(c / bm) tiles of at most bm consecutive sorted positions;
-// tiles are listed expert by expert.  The tile count goes to *num_tiles.
+// c = offsets[e+1]-offsets[e] pairs contributes ceil(c / bm) tiles of at most
+// bm consecutive sorted positions; tiles are listed expert by expert.  The tile
+// count goes to *num_tiles.
 __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restrict__ offsets,
                                                           int E,
                                                           int bm, Tile* __restrict__ tiles,
@@ -441,7 +442,8 @@ __global__ __launch_bounds__(256) void build_tiles_kernel(const int32_t* __restr
 
 hipError_t launch_build_tiles(const int32_t* offsets, int E, int bm, Tile* tiles,
                               int32_t* num_tiles, hipStream_t st, const RowQuant& rq) {
-  build_tiles_kernel<<<1 + row_quant_blocks(rq), 256, 0, st>>>(offsets, E, bm, tiles, num_tiles, rq);
+  build_tiles_kernel<<<1 + row_quant_blocks(rq), 256, 0, st>>>(offsets, E, bm, tiles, num_tiles,
+                                                               rq);
   return hipGetLastError();
 }
 
@@ -781,9 +783,9 @@ hipError_t launch_route_small(const float* logits, int T, int E, int k, int reno
   if (wg && ((long)T * E > kFusedRouterMaxTE || (long)E * H > kFusedRouterMaxEH || !x || H % 128))
     return hipErrorInvalidValue;
   // at most one of xq and rq
-  route_small_kernel<<<xq ? 2 : 1 + (int)rq.rows, 1024, 0, st>>>(logits, T, E, k, renorm, ids, w, counts,
-                                                 offsets, sorted_ids, inv_perm, bm, big ? 1 : 0,
-                                                 tiles, ctrl, x, H, xq, wg, logits_out, rq);
+  route_small_kernel<<<xq ? 2 : 1 + (int)rq.rows, 1024, 0, st>>>(
+      logits, T, E, k, renorm, ids, w, counts, offsets, sorted_ids, inv_perm, bm, big ? 1 : 0, tiles,
+      ctrl, x, H, xq, wg, logits_out, rq);
   return hipGetLastError();
 }
 

@@ -15,16 +15,17 @@
 //   plain softmax: d logits[e] = [e = id_j] w_j g_j - p_te S.
 //
 // Both directions are one pass over [T,E] fp32 rows and bound by HBM for
-// large batches (131072 x 256: loss 33 us, its gradient 41 us, 4.1 and 6.5 TB/s
-// with the logits partly in the last-level cache; both gradients with plain
-// softmax 51 us), by launch latency for small ones (16 x 64: 3.3 and 2.2 us of
+// large batches (131072 x 256 in a training step: loss 43 us, without its
+// arithmetic 38, since the step's last gradient is still being written back; its
+// gradient 42 us, 6.4 TB/s; 65536 x 256, a third of it padding, both gradients
+// with plain softmax 27 us, 4.4 TB/s), by launch latency for small ones (16 x 64: 3.7 and 2.4 us of
 // kernel under 7 us of host work per call).  L = 16 lanes hold a row of
 // up to 256 logits (four rows per wave), each lane NC runs of 4 values, so the
 // row reductions stay inside the 16-lane rows that DPP moves reach at full
 // rate; longer rows take 32 or 64 lanes rather than more registers per lane
-// (16 lanes of 64 values held one wave per SIMD: 1024 experts at 2.3 TB/s).  No sum depends
-// on scheduling: blocks write partial sums that one block adds in block
-// order, and the counts are integers.
+// (16 lanes of 64 values held one wave per SIMD: 1024 experts at 2.3 TB/s).
+// No sum depends on scheduling: blocks write partial sums that one block adds in
+// block order, and the counts are integers.
 #include "moe_common.h"
 
 namespace moe {
@@ -541,7 +542,7 @@ hipError_t launch_router_grad(const float* logits, const int32_t* ids, const flo
   long nb = ((long)T + rows - 1) / rows;
   if (nb > 2048) nb = 2048;
 #define MOE_GRAD_AS(L_, NC_, VEC_, SOFT_, GATE_)                                                 \
-  router_grad_kernel<L_, NC_, VEC_, SOFT_, GATE_><<<(int)nb, kGradThreads, 0, st>>>(                \
+  router_grad_kernel<L_, NC_, VEC_, SOFT_, GATE_><<<(int)nb, kGradThreads, 0, st>>>(               \
       logits, ids, weights, grad_weights, mask, counts, token_count, grad_loss, coef, renorm, T, \
       E, k, grad)
 #define MOE_GRAD(L_, NC_, VEC_)                      \
