@@ -246,7 +246,8 @@ int moe_act_quant_e4m3(const void* a, int64_t n, uint8_t* codes, float* scales, 
  *          rounded before that, so the codes lie in [-127, 127]
  *   scales [rows] fp32 out: fl32(amax / 127), the value of one code
  *          (amax = 0: scale 1, codes 0)
- * a holds no NaN and no infinity (precondition).  Null or misaligned (16 B)
+ * A row that holds a NaN or an infinity has scale NaN and no defined codes, so
+ * that every product with it is NaN.  Null or misaligned (16 B)
  * pointers, rows < 0 or >= 2^31, or n not a positive multiple of 8, give
  * MOE_ERR_INVALID_ARG; rows = 0 returns MOE_OK with nothing enqueued. */
 int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, float* scales,
@@ -267,8 +268,9 @@ int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, floa
  *   token_count   [1] int32 out: N
  *   ws, ws_bytes  workspace of moe_balance_loss_workspace_bytes, 256-byte
  *                 aligned; holds nothing after the call
- * A NaN logit is read as -inf (as the gating does), and a row without a
- * finite logit has probability 0 everywhere.  With N = 0 (also T = 0, where
+ * A NaN logit is read as -inf (as the gating does), a row of -inf only has
+ * probability 0 everywhere, and a counted row with +inf makes the loss and the
+ * probabilities (and its own gradient rows below) NaN.  With N = 0 (also T = 0, where
  * unlike in other calls the outputs are written) loss, counts and
  * probabilities are 0.  Sums over tokens are fp32 inside a block of rows and
  * fp64 across blocks, in a fixed order.  Errors as moe_align_sort. */

@@ -171,14 +171,14 @@ struct RowQuant {
 // least 2^-17 away from one, so the integer is the exact one.  A row whose
 // amax is below 2^-100 is scaled up by 2^64 first, since 127 / amax would
 // overflow.  The first THREADS * VPT vectors of 8 stay in registers between
-// the maximum and the codes, the others are read twice.
-__device__ __forceinline__ float bf16x8_amax(i32x4 v) {
-  float m = 0.f;
+// the maximum and the codes, the others are read twice.  The maximum is taken
+// on the values' bits, two 16-bit ones at a time: |a| orders like its bits, and
+// a NaN, above infinity there, is not lost as it is in fmaxf.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u16x2 bf16x8_amax(u16x2 m, i32x4 v) {
 #pragma unroll
-  for (int q = 0; q < 4; q++) {
-    const uint32_t u = (uint32_t)v[q];
-    m = fmaxf(m, fmaxf(fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xffff0000u))));
-  }
+  for (int q = 0; q < 4; q++)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[q] & 0x7fff7fff));
   return m;
 }
 
@@ -201,30 +201,34 @@ __device__ __forceinline__ uint2 bf16x8_to_i8x8(i32x4 v, float up, float r, floa
 
 template <int THREADS, int VPT>
 __device__ __forceinline__ void quant_i8_row(const RowQuant& rq, long row) {
-  __shared__ float part[THREADS / kWave];
+  __shared__ uint32_t part[THREADS / kWave];
   const int t = threadIdx.x;
   const i32x4* s4 = reinterpret_cast<const i32x4*>(rq.src) + row * rq.n8;
   uint2* d2 = reinterpret_cast<uint2*>(rq.codes) + row * rq.n8;
   i32x4 v[VPT];
-  float m = 0.f;
+  u16x2 m2 = {0, 0};
 #pragma unroll
   for (int u = 0; u < VPT; u++) {
     const int i = t + u * THREADS;
     v[u] = i < rq.n8 ? s4[i] : i32x4{0, 0, 0, 0};
   }
 #pragma unroll
-  for (int u = 0; u < VPT; u++) m = fmaxf(m, bf16x8_amax(v[u]));
-  for (int i = t + VPT * THREADS; i < rq.n8; i += THREADS) m = fmaxf(m, bf16x8_amax(s4[i]));
-  m = wave_max(m);
-  if (lane_id() == 0) part[t / kWave] = m;
-  __syncthreads();
-  m = part[0];
+  for (int u = 0; u < VPT; u++) m2 = bf16x8_amax(m2, v[u]);
+  for (int i = t + VPT * THREADS; i < rq.n8; i += THREADS) m2 = bf16x8_amax(m2, s4[i]);
+  uint32_t bits = max(m2[0], m2[1]);
 #pragma unroll
-  for (int w = 1; w < THREADS / kWave; w++) m = fmaxf(m, part[w]);
+  for (int o = 32; o > 0; o >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, o));
+  if (lane_id() == 0) part[t / kWave] = bits;
+  __syncthreads();
+  bits = part[0];
+#pragma unroll
+  for (int w = 1; w < THREADS / kWave; w++) bits = max(bits, part[w]);
+  const float m = __uint_as_float(bits << 16);
   const float up = m < 0x1p-100f ? 0x1p64f : 1.0f, mu = m * up;
   const float r = mu > 0.f ? 127.0f / mu : 0.f;
   const float r_lo = mu > 0.f ? fmaf(-r, mu, 127.0f) / mu : 0.f;
-  if (t == 0) rq.scales[row] = m > 0.f ? m / 127.0f : 1.0f;
+  // a row with NaN or an infinity has no codes: its products are NaN
+  if (t == 0) rq.scales[row] = m == 0.f ? 1.0f : m < INFINITY ? m / 127.0f : NAN;
 #pragma unroll
   for (int u = 0; u < VPT; u++) {
     const int i = t + u * THREADS;

@@ -108,8 +108,8 @@ __device__ __forceinline__ float exp_neg(float x) {
   return fmaf(e, lost * kLn2, e);
 }
 
-// Softmax of a row in place; NaN reads as -inf (as the gating reads it), and
-// a row without a finite logit becomes all zero.
+// Softmax of a row in place; NaN reads as -inf (as the gating reads it), a row
+// of -inf only becomes all zero, and a row with +inf all NaN.
 template <int L, int N>
 __device__ __forceinline__ void softmax_row(float (&v)[N]) {
   float m = -INFINITY;
@@ -127,7 +127,7 @@ __device__ __forceinline__ void softmax_row(float (&v)[N]) {
     s += v[q];
   }
   s = row_sum<L>(s);
-  const float inv = s > 0.f ? 1.0f / s : 0.f;
+  const float inv = s > 0.f ? 1.0f / s : m == INFINITY ? NAN : 0.f;
 #pragma unroll
   for (int q = 0; q < N; q++) v[q] *= inv;
 }

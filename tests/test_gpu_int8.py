@@ -67,6 +67,37 @@ def test_row_codes_over_the_whole_range():
     assert np.array_equal(scales.cpu().numpy().view(np.uint32), ws.view(np.uint32))
 
 
+@pytest.mark.parametrize("n", [8, 2048, 20000])
+def test_row_codes_of_nan_and_infinity(n):
+    a = torch.ones(6, n, dtype=torch.bfloat16)
+    for row, bad in ((1, np.nan), (2, np.inf), (3, -np.inf), (4, -np.nan)):
+        a[row, n - row] = bad
+    scales = moe.moe_act_quant_i8(a.cuda())[1].cpu()
+    assert bool(torch.isnan(scales[1:5]).all())
+    assert bool((scales[[0, 5]] == np.float32(1) / np.float32(127)).all())
+
+
+@pytest.mark.parametrize("T,E,k,I", [(3, 8, 2, 256), (200, 4, 2, 128), (2100, 4, 2, 8192)])
+def test_nan_and_infinity_in_x_reach_their_tokens_only(T, E, k, I):
+    """Few-token kernel, 64- and 256-position tiles: the outputs of two tokens
+    are NaN, the others are what they are without those tokens' values."""
+    say("NaN and infinity in x", T, E, k, I)
+    H = 256
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    w13 = torch.randint(-127, 128, (E, 2 * I, H), generator=g, device="cuda").to(torch.int8)
+    w2 = torch.randint(-127, 128, (E, H, I), generator=g, device="cuda").to(torch.int8)
+    s13 = torch.rand(E, 2 * I, generator=g, device="cuda") * 1e-3
+    s2 = torch.rand(E, H, generator=g, device="cuda") * 1e-3
+    want = moe.moe_fused_forward(x, logits, w13, s13, w2, s2, k)
+    x[0, 5] = np.nan
+    x[T - 1, 255] = -np.inf
+    got = moe.moe_fused_forward(x, logits, w13, s13, w2, s2, k)
+    assert bool(torch.isnan(got[0]).all()) and bool(torch.isnan(got[T - 1]).all())
+    assert torch.equal(got[1:T - 1], want[1:T - 1])
+
+
 def test_row_codes_of_many_rows():
     """2^24 + 5 rows, and the last of them: a block per row would be 2^32 threads."""
     say("row codes of many rows")

@@ -100,6 +100,37 @@ def test_gating_and_router_gradients(T, E, k, masked, renorm):
     _within(both.cpu().numpy(), want + more, bound, "router gradient")
 
 
+@pytest.mark.parametrize("E", [16, 61, 600])
+def test_a_logit_of_plus_infinity_is_not_hidden(E):
+    """Its row has no softmax: loss and probabilities are NaN, and so is the
+    row's gradient where the softmax enters it; the other rows keep theirs."""
+    T, k = 40, 2
+    g, logits, ids, _ = _inputs(T, E, k, E, False)
+    counts = np.bincount(ids.reshape(-1), minlength=E).astype(np.int32)
+    w = np.full((T, k), 0.5, np.float32)
+    gw = g.standard_normal((T, k)).astype(np.float32)
+    one, n = torch.ones(1, device="cuda"), _dev(np.array([T], np.int32))
+
+    def grads(l):
+        return [moe.moe_balance_loss_backward(l, _dev(counts), n, k, 1.0, one).cpu().numpy(),
+                moe.moe_topk_gating_backward(l, _dev(ids), _dev(w), _dev(gw),
+                                             renormalize=False).cpu().numpy()]
+
+    want = grads(_dev(logits))
+    logits[17, 3] = np.inf
+    dl = _dev(logits)
+    loss, c, probs, tokens = moe.moe_balance_loss(dl, _dev(ids), 1.0)
+    assert bool(torch.isnan(loss).all()) and bool(torch.isnan(probs).all())
+    assert np.array_equal(c.cpu().numpy(), counts) and int(tokens) == T
+    for got, ref in zip(grads(dl), want):
+        assert np.all(np.isnan(got[17]))
+        rest = np.arange(T) != 17
+        assert np.array_equal(got[rest], ref[rest])
+    mask = np.ones(T, np.uint8)
+    mask[17] = 0
+    assert bool(torch.isfinite(moe.moe_balance_loss(dl, _dev(ids), 1.0, token_mask=_dev(mask))[0]))
+
+
 @pytest.mark.parametrize("E", [16, 61, 256])
 def test_rows_without_a_finite_logit_nan_and_infinities(E):
     """-inf and NaN logits, rows with nothing left, NaN and infinities in rows
