@@ -18,7 +18,7 @@
 // fragments are read under this step's MFMAs, and the one barrier of a stage
 // sits a K step before its end, with 16 MFMAs still to issue behind it.
 //
-// Measured (one box; large_i8 kernel alone): 8 experts of 2048 pairs, 28672 x
+// Measured (one card; large_i8 kernel alone): 8 experts of 2048 pairs, 28672 x
 // 4096 gate/up (3.85 Tops) 1.77 ms, 2.17 Pop/s; a square library product of the
 // same type (16384 x 16384 x 8192) reaches 2.13 Pop/s on that card.  Bound by the
 // matrix units at the clock the power limit leaves: without the epilogue 5%
