@@ -175,6 +175,7 @@ def _check_i8(x, x_name, width, w, w_name, scale, ids=()):
     dev = _gpu(x, x_name)
     _need(dev == _current_device(), "%s must live on the current GPU" % x_name)
     _need(w.dim() == 3 and w.shape[2] == width, "%s must be [E, channels, %d]" % (w_name, width))
+    _need(w_name != "w13" or w.shape[1] % 2 == 0, "w13 must hold as many gate as up rows")
     _arg(x, x_name, torch.bfloat16, (x.shape[0], width), dev)
     _arg(w, w_name, torch.int8, w.shape, dev)
     _need(scale is not None, "%s_scale is required in INT8 mode" % w_name)

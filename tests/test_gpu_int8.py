@@ -424,7 +424,9 @@ def test_refusals_on_the_gpu():
     for bad in ((x.float(), lg, w13, s13, w2, s2), (x, lg, w13, s13[:, 0].contiguous(), w2, s2),
                 (x, lg, w13, s13, w2, s2[:, 0].contiguous()), (x, lg, w13, None, w2, s2),
                 (x, lg, w13, s13, w2.view(torch.uint8), s2), (x, lg, w13, s13.double(), w2, s2),
-                (x, lg.double(), w13, s13, w2, s2), (x, lg, w13, s13, w2[:4], s2[:4])):
+                (x, lg.double(), w13, s13, w2, s2), (x, lg, w13, s13, w2[:4], s2[:4]),
+                (x, lg, torch.zeros(8, 513, 256, dtype=torch.int8, device="cuda"),
+                 torch.ones(8, 513, device="cuda"), w2, s2)):
         with pytest.raises(moe.MoeError):
             moe.moe_fused_forward(*bad, 2)
     with pytest.raises(moe.MoeError):
