@@ -46,11 +46,10 @@
  *                  expert and output channel (w13_scale [E,2I], w2_scale
  *                  [E,H]); x and h are quantised to int8 inside the layer with
  *                  one dynamic scale per row (moe_act_quant_i8); the products
- *                  of codes are summed exactly in 32-bit integers.  Where y
- *                  holds 2^24 values or more (T k H) and experts many pairs,
- *                  the fused entry points round it to bf16 before the
- *                  aggregation.  H and I are at most 131072 in this mode
- *                  (MOE_ERR_UNSUPPORTED), so that no such sum overflows.
+ *                  of codes are summed exactly in 32-bit integers; y is fp32
+ *                  in the fused entry points too.  H and I are at most 131072
+ *                  in this mode (MOE_ERR_UNSUPPORTED), so that no such sum
+ *                  overflows.
  * Layouts (row-major, last index contiguous):
  *   x [T,H]; logits [T,E] fp32; w13 [E,2I,H] (rows 0..I-1 gate, I..2I-1 up);
  *   w2 [E,H,I]; h [T*k,I] and y [T*k,H] in expert-sorted pair order;

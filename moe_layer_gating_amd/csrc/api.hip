@@ -761,11 +761,9 @@ int fused_impl(const moe_shape* s, const void* x, const float* logits, const voi
   }
   // FP8 layers with many tokens per expert keep y in bf16 between the down
   // projection and the aggregation (half the bytes of that round trip); the
-  // step entry points return fp32 y.  INT8 layers do where y is large (an
-  // output then carries two bf16 roundings, 1.4 times the error of one; 4096
-  // tokens, k 8, H 7168: 0.2 ms of 2.8 ms saved) and keep it in fp32 below
-  // 2^24 values, where the round trip is a few us.
-  const bool y_bf16 = (fp8 && big) || (i8 && big && (long)T * k * H >= 1L << 24);
+  // step entry points return fp32 y.  INT8 layers keep it in fp32 at every
+  // size: rounded twice, an output's error grew from 1.7e-3 to 2.3e-3.
+  const bool y_bf16 = fp8 && big;
   if (big)
     MOE_TRY(launch_w2_tiles(s->wdtype, tiles_bm(*s), bh, w2, w2_scale, tiles_w2,
                             &ctrl->num_tiles_big, (int)L.max_tiles_big, H, I, act_h, y, y_bf16,

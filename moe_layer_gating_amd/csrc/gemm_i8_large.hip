@@ -289,10 +289,10 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
                  (size_t)I * 2);
 }
 
-template <int ROWS, int NPOS, int BM, bool YB>
+template <int ROWS, int NPOS, int BM>
 __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, const float* w2_scale,
                                               const Tile& tl, int nb, int H, int I,
-                                              const float* hs, void* y, LargeLds<ROWS, BM>& L) {
+                                              const float* hs, float* y, LargeLds<ROWS, BM>& L) {
   typedef LargeShape<ROWS, NPOS> S;
   const int t = threadIdx.x, lane = lane_id(), w = t / kWave;
   constexpr int NA = ROWS / 32;
@@ -331,9 +331,9 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
   float sh[S::CT];
 #pragma unroll
   for (int j = 0; j < S::CT; j++) sh[j] = L.as[(wc * S::CT + j) * 32 + r32];
-  // a position's row in LDS holds at most 512 bytes: every channel, or 256
-  // fp32 channels in two passes (half of each wave's row tiles)
-  constexpr int ES = YB ? 2 : 4, PASSES = ROWS * ES > 512 ? 2 : 1, RP = S::RT / PASSES;
+  // a position's row in LDS holds 512 bytes: 128 channels, 256 in two passes
+  // (half of each wave's row tiles)
+  constexpr int ES = 4, PASSES = ROWS * ES > 512 ? 2 : 1, RP = S::RT / PASSES;
   constexpr int ROWB = ROWS * ES / PASSES, CH = ROWB / 16;
 #pragma unroll
   for (int pass = 0; pass < PASSES; pass++) {
@@ -352,12 +352,8 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
           for (int u = 0; u < 4; u++)
             v[u] = (float)acc[pass * RP + i][j][4 * q + u] * (ws[u] * sh[j]);
           const int p = (wc * S::CT + j) * 32 + r32;
-          char* dst = L.buf + p * ROWB + (((o >> 4) ^ (p & (CH - 1))) << 4) + (o & 15);
-          if (YB)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-          else
-            *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+          *reinterpret_cast<f32x4*>(L.buf + p * ROWB + (((o >> 4) ^ (p & (CH - 1))) << 4)) =
+              f32x4{v[0], v[1], v[2], v[3]};
         }
       }
     __syncthreads();
@@ -367,9 +363,8 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
       const int p = i / CH, c = i % CH;
       const int ch = nb * ROWS + (c / SEG * S::RT + pass * RP) * 32 + c % SEG * 16 / ES;
       if (ch < H)
-        *reinterpret_cast<uint4*>(reinterpret_cast<char*>(y) +
-                                  ((size_t)(tl.p0 + p) * H + ch) * ES) =
-            *reinterpret_cast<const uint4*>(L.buf + p * ROWB + ((c ^ (p & (CH - 1))) << 4));
+        *reinterpret_cast<f32x4*>(y + (size_t)(tl.p0 + p) * H + ch) =
+            *reinterpret_cast<const f32x4*>(L.buf + p * ROWB + ((c ^ (p & (CH - 1))) << 4));
     }
   }
 }
@@ -436,19 +431,19 @@ __attribute__((amdgpu_waves_per_eu(BM == 64 ? 2 : 1, BM == 64 ? 2 : 1))) void w1
   });
 }
 
-template <int BM, bool YB>
+template <int BM>
 __global__ __launch_bounds__(256)
 __attribute__((amdgpu_waves_per_eu(BM == 64 ? 2 : 1, BM == 64 ? 2 : 1))) void w2_large_i8(
     const char* __restrict__ b, const char* __restrict__ w2, const float* __restrict__ w2_scale,
     const Tile* __restrict__ tiles, const int32_t* __restrict__ num_tiles, int H, int I,
-    const float* __restrict__ hs, void* __restrict__ y) {
+    const float* __restrict__ hs, float* __restrict__ y) {
   constexpr int ROWS = large_rows<BM>();
   __shared__ __attribute__((aligned(16))) LargeLds<ROWS, BM> L;
   Tile tl;
   int nb;
   if (!large_work<BM>(tiles, num_tiles, (H + ROWS - 1) / ROWS, &tl, &nb)) return;
   by_width<BM>(tl.mt, [&](auto n) {
-    w2_large_tile<ROWS, n.value, BM, YB>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
+    w2_large_tile<ROWS, n.value, BM>(b, w2, w2_scale, tl, nb, H, I, hs, y, L);
   });
 }
 
@@ -471,13 +466,11 @@ hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const flo
 
 hipError_t launch_w2_large_i8(int bm, const void* b, const void* w2, const float* w2_scale,
                               const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
-                              int I, const float* hs, void* y, bool y_bf16, hipEvent_t e0,
-                              hipEvent_t e1, hipStream_t st) {
-  const auto kern = bm == 64 ? (y_bf16 ? w2_large_i8<64, true> : w2_large_i8<64, false>)
-                             : (y_bf16 ? w2_large_i8<256, true> : w2_large_i8<256, false>);
-  launch_on(kern, dim3(large_grid(bm, max_tiles, H)), dim3(256), st, e0, e1,
-            reinterpret_cast<const char*>(b), reinterpret_cast<const char*>(w2), w2_scale, tiles,
-            num_tiles, H, I, hs, y);
+                              int I, const float* hs, float* y, hipEvent_t e0, hipEvent_t e1,
+                              hipStream_t st) {
+  launch_on(bm == 64 ? w2_large_i8<64> : w2_large_i8<256>, dim3(large_grid(bm, max_tiles, H)),
+            dim3(256), st, e0, e1, reinterpret_cast<const char*>(b),
+            reinterpret_cast<const char*>(w2), w2_scale, tiles, num_tiles, H, I, hs, y);
   return hipGetLastError();
 }
 

@@ -327,7 +327,7 @@ hipError_t launch_w13_tiles(int mode, int bm, const void* b, const void* w13,
                             const int32_t* num_tiles, int max_tiles, int H, int I, int k,
                             const uint32_t* act_amax_bits, void* h, uint32_t* amax_h_bits,
                             hipEvent_t e0, hipEvent_t e1, hipStream_t st);
-// y_bf16 (FP8 and INT8 only): y is stored in bf16 instead of fp32.
+// y_bf16 (FP8 only): y is stored in bf16 instead of fp32.
 hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, const float* w2_scale,
                            const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
                            int I, const uint32_t* act_amax_bits, void* y, bool y_bf16,
@@ -341,8 +341,8 @@ hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const flo
                                hipStream_t st);
 hipError_t launch_w2_large_i8(int bm, const void* b, const void* w2, const float* w2_scale,
                               const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
-                              int I, const float* hs, void* y, bool y_bf16, hipEvent_t e0,
-                              hipEvent_t e1, hipStream_t st);
+                              int I, const float* hs, float* y, hipEvent_t e0, hipEvent_t e1,
+                              hipStream_t st);
 // Inverse rotary embedding + per-head e4m3 quantisation (rope.hip); shapes
 // already checked by the caller (head_dim / 8 <= 64 lanes per head).
 hipError_t launch_inv_rope_fp8(const uint16_t* x, const int32_t* positions, const float* cos_sin,
