@@ -296,13 +296,16 @@ int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
  *   renormalize = 0: grad_logits[e] = (e = id_j ? w_j g_j : 0) - p_e S, p the
  *                    softmax over all experts.
  *   topk_ids [T,k], topk_weights [T,k] as moe_topk_gating wrote them;
- *   grad_weights [T,k] fp32; logits [T,E] (read with renormalize = 0 only,
- *   may be NULL otherwise); token_mask as above (a token that does not count
+ *   grad_weights [T,k] fp32; logits [T,E] (with renormalize = 1 read for rows
+ *   with a NaN weight only, and may be NULL); token_mask as above (a token that does not count
  *   gets a zero row); grad_logits [T,E] fp32 out, every row written, not
  *   overlapping an input.
- * A slot whose id lies outside [0, E) contributes nothing, slots that name
- * one expert twice add up in slot order, and a NaN weight (the gating of a
- * row without a finite logit) counts as 0.  Errors as moe_topk_gating. */
+ * A slot whose id lies outside [0, E) contributes nothing, and slots that name
+ * one expert twice add up in slot order.  A NaN weight counts as 0 (the gating
+ * of a row without a finite logit), but a row whose logits hold +inf, for which
+ * the gating gives NaN weights too, has a gradient of NaN; without logits the
+ * two cannot be told apart, and a NaN weight counts as 0.  Errors as
+ * moe_topk_gating. */
 int moe_topk_gating_backward(const float* logits, const int32_t* topk_ids,
                              const float* topk_weights, const float* grad_weights,
                              const uint8_t* token_mask, int32_t T, int32_t E, int32_t k,

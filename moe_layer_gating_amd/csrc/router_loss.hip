@@ -336,6 +336,9 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(
 // A selected expert's term reaches the lane that owns the expert through the
 // row's LDS copy: the lane of slot j adds the terms of every slot naming the
 // same expert in slot order, and the first of those slots writes the sum.
+// A row with NaN weights is one that the gating found no finite maximum in: its
+// terms are 0 if it holds no +inf, else its gradient is NaN.  Where the softmax
+// is not formed, such a row's logits are looked at for that alone.
 template <int L, int NC, bool VEC, bool SOFT, bool GATE>
 __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
@@ -390,19 +393,29 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
     if (SOFT && on1) load_row<L, NC, VEC>(logits + (size_t)(r + step) * E, E, l, next, -INFINITY);
     float S = 0.f;
     int id = -1;
+    bool lost = false;  // !SOFT: the row's gradient is NaN
     if (GATE) {
       float wg = 0.f, wj = 0.f;
+      bool nan_w = false;
       if (on && l < k) {
         const size_t f = (size_t)r * k + l;
         id = ids[f];
         wj = weights[f];
         const float gj = grad_weights[f];
-        wj = wj == wj ? wj : 0.f;  // the gating of a row without a finite logit
+        nan_w = wj != wj;
+        wj = nan_w ? 0.f : wj;
         wg = wj * gj;
         if ((unsigned)id >= (unsigned)E) {
           id = -1;
           wj = wg = 0.f;
         }
+      }
+      if (!SOFT && __any(nan_w && logits)) {  // the same way for the whole wave
+        float m = -INFINITY;
+        if (on)
+          for (int e = l; e < E; e += L) m = fmaxf(m, logits[(size_t)r * E + e]);
+        m = row_max<L>(m);
+        lost = row_max<L>(nan_w ? 1.f : 0.f) > 0.f && m == INFINITY;
       }
       S = row_sum<L>(wg);
       const float term = renorm ? wg - wj * S : wg;
@@ -442,6 +455,10 @@ __global__ __launch_bounds__(kGradThreads) void router_grad_kernel(
             for (int i = 0; i < 4; i++)
               v[4 * c + i] = (SOFT ? v[4 * c + i] : 0.f) + sel[g][expert_of<L, false>(c, i, l)];
           }
+        }
+        if (!SOFT && lost) {
+#pragma unroll
+          for (int q = 0; q < N; q++) v[q] = NAN;
         }
       }
     } else {
