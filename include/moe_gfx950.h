@@ -283,8 +283,8 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
  *   grad_logits[t][i] = grad_loss coef E / N * p_ti (f_i - sum_e f_e p_te)
  * for the tokens that count, 0 for the others.  expert_counts, token_count,
  * token_mask and coef as in the forward call; grad_loss [1] fp32 on the
- * device; grad_logits [T,E] fp32 out, every row written, not overlapping an
- * input.  Errors as moe_topk_gating. */
+ * device; grad_logits [T,E] fp32 out, every row written.  Errors as
+ * moe_topk_gating, and MOE_ERR_INVALID_ARG where grad_logits overlaps an input. */
 int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
                               const int32_t* expert_counts, const int32_t* token_count, int32_t T,
                               int32_t E, int32_t k, float coef, const float* grad_loss,
@@ -298,8 +298,8 @@ int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
  *   topk_ids [T,k], topk_weights [T,k] as moe_topk_gating wrote them;
  *   grad_weights [T,k] fp32; logits [T,E] (with renormalize = 1 read for rows
  *   with a NaN weight only, and may be NULL); token_mask as above (a token that does not count
- *   gets a zero row); grad_logits [T,E] fp32 out, every row written, not
- *   overlapping an input.
+ *   gets a zero row); grad_logits [T,E] fp32 out, every row written
+ *   (MOE_ERR_INVALID_ARG where it overlaps an input).
  * A slot whose id lies outside [0, E) contributes nothing, and slots that name
  * one expert twice add up in slot order.  A NaN weight counts as 0 (the gating
  * of a row without a finite logit), but a row whose logits hold +inf, for which

@@ -404,21 +404,14 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=
     return loss, expert_counts, expert_probs, token_count
 
 
-def _grad_buffer(grad_logits, logits, shape, dev):
-    if grad_logits is None:
-        return torch.empty(shape, dtype=torch.float32, device=dev)
-    _need(grad_logits.data_ptr() != logits.data_ptr() or grad_logits.numel() == 0,
-          "grad_logits must not overlap logits")
-    return grad_logits
-
-
 def moe_balance_loss_backward(logits, expert_counts, token_count, k, coef, grad_loss,
                               token_mask=None, grad_logits=None):
     """Gradient [T,E] of moe_balance_loss on the logits, from the counts it
     returned; grad_loss [1] fp32."""
     dev = _gpu(logits, "logits")
     T, E = shape = logits.shape
-    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(shape, dtype=torch.float32, device=dev)
     _run("moe_balance_loss_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
          _mask_arg(token_mask, T, dev),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
@@ -436,7 +429,8 @@ def moe_topk_gating_backward(logits, topk_ids, topk_weights, grad_weights, renor
     T, E = shape = logits.shape
     k = topk_ids.shape[-1]
     pairs = (T, k)
-    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(shape, dtype=torch.float32, device=dev)
     _run("moe_topk_gating_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
          _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
          _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),
@@ -453,7 +447,8 @@ def moe_router_backward(logits, topk_ids, topk_weights, grad_weights, expert_cou
     T, E = shape = logits.shape
     k = topk_ids.shape[-1]
     pairs = (T, k)
-    grad_logits = _grad_buffer(grad_logits, logits, shape, dev)
+    if grad_logits is None:
+        grad_logits = torch.empty(shape, dtype=torch.float32, device=dev)
     _run("moe_router_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
          _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
          _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),

@@ -189,6 +189,25 @@ int check_ws(const moe_shape* s, void* ws, size_t ws_bytes) {
   return MOE_OK;
 }
 
+// Whether [a, a + na) and [b, b + nb) share a byte; NULL shares none.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+// Whether the gradient rows written at grad share a byte with what the router
+// gradients read (NULL where an entry point has no such argument).
+inline bool grad_overlaps(const float* grad, int T, int E, int k, const float* logits,
+                          const int32_t* ids, const float* weights, const float* grad_weights,
+                          const uint8_t* mask, const int32_t* counts, const int32_t* token_count,
+                          const float* grad_loss) {
+  const size_t n = (size_t)T * E * 4, pairs = (size_t)T * k * 4;
+  return overlap(grad, n, logits, n) || overlap(grad, n, ids, pairs) ||
+         overlap(grad, n, weights, pairs) || overlap(grad, n, grad_weights, pairs) ||
+         overlap(grad, n, mask, T) || overlap(grad, n, counts, (size_t)E * 4) ||
+         overlap(grad, n, token_count, 4) || overlap(grad, n, grad_loss, 4);
+}
+
 inline int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
 #define MOE_TRY(expr)                         \
@@ -506,6 +525,9 @@ int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
   if (!aligned16(logits) || !aligned16(token_mask) || !aligned16(expert_counts) ||
       !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
     return MOE_ERR_INVALID_ARG;
+  if (grad_overlaps(grad_logits, T, E, k, logits, nullptr, nullptr, nullptr, token_mask,
+                    expert_counts, token_count, grad_loss))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_router_grad(logits, nullptr, nullptr, nullptr, token_mask,
                                        expert_counts, token_count, grad_loss, coef, 1, T, E, k,
                                        grad_logits, reinterpret_cast<hipStream_t>(stream)));
@@ -523,6 +545,9 @@ int moe_topk_gating_backward(const float* logits, const int32_t* topk_ids,
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
       !aligned16(grad_weights) || !aligned16(token_mask) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_overlaps(grad_logits, T, E, k, logits, topk_ids, topk_weights, grad_weights, token_mask,
+                    nullptr, nullptr, nullptr))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_router_grad(logits, topk_ids, topk_weights, grad_weights, token_mask,
                                        nullptr, nullptr, nullptr, 0.f, renormalize, T, E, k,
@@ -544,6 +569,9 @@ int moe_router_backward(const float* logits, const int32_t* topk_ids, const floa
   if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
       !aligned16(grad_weights) || !aligned16(token_mask) || !aligned16(expert_counts) ||
       !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
+    return MOE_ERR_INVALID_ARG;
+  if (grad_overlaps(grad_logits, T, E, k, logits, topk_ids, topk_weights, grad_weights, token_mask,
+                    expert_counts, token_count, grad_loss))
     return MOE_ERR_INVALID_ARG;
   return hip_status(launch_router_grad(logits, topk_ids, topk_weights, grad_weights, token_mask,
                                        expert_counts, token_count, grad_loss, coef, renormalize,
