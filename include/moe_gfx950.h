@@ -272,7 +272,11 @@ int moe_act_quant_i8(const void* a, int64_t rows, int32_t n, int8_t* codes, floa
  * probabilities (and its own gradient rows below) NaN.  With N = 0 (also T = 0, where
  * unlike in other calls the outputs are written) loss, counts and
  * probabilities are 0.  Sums over tokens are fp32 inside a block of rows and
- * fp64 across blocks, in a fixed order.  Errors as moe_align_sort. */
+ * fp64 across blocks, in a fixed order.
+ * Here and in the gradients below the one-word values (loss, token_count,
+ * grad_loss) may lie on any 4-byte address, and so may expert_counts and
+ * expert_probs where E is no multiple of 4: an element or a row of a tensor
+ * that holds one per layer.  Errors as moe_align_sort. */
 size_t moe_balance_loss_workspace_bytes(int32_t T, int32_t k, int32_t E);
 int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
                      int32_t T, int32_t E, int32_t k, float coef, float* loss,

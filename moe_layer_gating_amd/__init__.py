@@ -141,12 +141,18 @@ def _arg(t, name, dtype, shape, dev):
     return t.data_ptr()
 
 
-def _mask_arg(t, T, dev):
+def _aligned_mask(t, T, dev):
+    """A token mask the library takes: a slice of a longer one, which may start
+    at any byte, is copied to an aligned address."""
     if t is None:
         return None
     _need(t.dtype is torch.uint8 or t.dtype is torch.bool,
           "token_mask must be uint8 or bool, got %s" % t.dtype)
-    return _arg(t, "token_mask", t.dtype, (T,), dev)
+    return t.clone() if _arg(t, "token_mask", t.dtype, (T,), dev) & 15 else t
+
+
+def _mask_ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _gpu(t, name):
@@ -379,9 +385,11 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=
     """Load-balance loss coef * E * sum_e f_e P_e of the router logits [T,E]
     and the chosen experts topk_ids [T,k].  token_mask [T] (uint8 or bool,
     0 = padding) leaves tokens out.  Returns (loss [1] fp32, expert_counts
-    [E] int32, expert_probs [E] fp32, token_count [1] int32)."""
+    [E] int32, expert_probs [E] fp32, token_count [1] int32).  A mask that is
+    not 16-byte aligned is copied first."""
     dev = _gpu(logits, "logits")
     T, E = shape = logits.shape
+    token_mask = _aligned_mask(token_mask, T, dev)
     k = topk_ids.shape[-1]
     pairs = (T, k)
     if ws is None:
@@ -395,7 +403,7 @@ def moe_balance_loss(logits, topk_ids, coef=1.0, token_mask=None, ws=None, loss=
     if token_count is None:
         token_count = torch.empty(1, dtype=torch.int32, device=dev)
     _run("moe_balance_loss", dev, _arg(logits, "logits", torch.float32, shape, dev),
-         _arg(topk_ids, "topk_ids", torch.int32, pairs, dev), _mask_arg(token_mask, T, dev), T, E,
+         _arg(topk_ids, "topk_ids", torch.int32, pairs, dev), _mask_ptr(token_mask), T, E,
          k, coef, _arg(loss, "loss", torch.float32, (1,), dev),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(expert_probs, "expert_probs", torch.float32, (E,), dev),
@@ -410,10 +418,11 @@ def moe_balance_loss_backward(logits, expert_counts, token_count, k, coef, grad_
     returned; grad_loss [1] fp32."""
     dev = _gpu(logits, "logits")
     T, E = shape = logits.shape
+    token_mask = _aligned_mask(token_mask, T, dev)
     if grad_logits is None:
         grad_logits = torch.empty(shape, dtype=torch.float32, device=dev)
     _run("moe_balance_loss_backward", dev, _arg(logits, "logits", torch.float32, shape, dev),
-         _mask_arg(token_mask, T, dev),
+         _mask_ptr(token_mask),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k, coef,
          _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),
@@ -427,6 +436,7 @@ def moe_topk_gating_backward(logits, topk_ids, topk_weights, grad_weights, renor
     returned, from grad_weights [T,k]."""
     dev = _gpu(logits, "logits")
     T, E = shape = logits.shape
+    token_mask = _aligned_mask(token_mask, T, dev)
     k = topk_ids.shape[-1]
     pairs = (T, k)
     if grad_logits is None:
@@ -435,7 +445,7 @@ def moe_topk_gating_backward(logits, topk_ids, topk_weights, grad_weights, renor
          _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
          _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),
          _arg(grad_weights, "grad_weights", torch.float32, pairs, dev),
-         _mask_arg(token_mask, T, dev), T, E, k, int(bool(renormalize)),
+         _mask_ptr(token_mask), T, E, k, int(bool(renormalize)),
          _arg(grad_logits, "grad_logits", torch.float32, shape, dev))
     return grad_logits
 
@@ -445,6 +455,7 @@ def moe_router_backward(logits, topk_ids, topk_weights, grad_weights, expert_cou
     """moe_topk_gating_backward plus moe_balance_loss_backward in one pass."""
     dev = _gpu(logits, "logits")
     T, E = shape = logits.shape
+    token_mask = _aligned_mask(token_mask, T, dev)
     k = topk_ids.shape[-1]
     pairs = (T, k)
     if grad_logits is None:
@@ -453,7 +464,7 @@ def moe_router_backward(logits, topk_ids, topk_weights, grad_weights, expert_cou
          _arg(topk_ids, "topk_ids", torch.int32, pairs, dev),
          _arg(topk_weights, "topk_weights", torch.float32, pairs, dev),
          _arg(grad_weights, "grad_weights", torch.float32, pairs, dev),
-         _mask_arg(token_mask, T, dev),
+         _mask_ptr(token_mask),
          _arg(expert_counts, "expert_counts", torch.int32, (E,), dev),
          _arg(token_count, "token_count", torch.int32, (1,), dev), T, E, k,
          int(bool(renormalize)), coef, _arg(grad_loss, "grad_loss", torch.float32, (1,), dev),

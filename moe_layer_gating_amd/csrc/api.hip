@@ -27,6 +27,11 @@ namespace {
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// a value per expert: read 16 bytes at a time where E is a multiple of 4
+inline bool aligned_experts(const void* p, int E) {
+  return E % 4 == 0 ? aligned16(p) : aligned4(p);
+}
 
 inline int act_bytes(int wdtype) { return wdtype == MOE_F32 ? 4 : 2; }
 
@@ -500,8 +505,9 @@ int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t
   if (rc) return rc;
   if (!loss || !expert_counts || !expert_probs || !token_count) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!logits || !topk_ids)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) || !aligned16(loss) ||
-      !aligned16(expert_counts) || !aligned16(expert_probs) || !aligned16(token_count))
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(token_mask) || !aligned4(loss) ||
+      !aligned_experts(expert_counts, E) || !aligned_experts(expert_probs, E) ||
+      !aligned4(token_count))
     return MOE_ERR_INVALID_ARG;
   const LossLayout L = loss_layout_for(T, E);
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < L.total)
@@ -522,8 +528,8 @@ int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask,
   if (T == 0) return MOE_OK;
   if (!logits || !expert_counts || !token_count || !grad_loss || !grad_logits)
     return MOE_ERR_INVALID_ARG;
-  if (!aligned16(logits) || !aligned16(token_mask) || !aligned16(expert_counts) ||
-      !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
+  if (!aligned16(logits) || !aligned16(token_mask) || !aligned_experts(expert_counts, E) ||
+      !aligned4(token_count) || !aligned4(grad_loss) || !aligned16(grad_logits))
     return MOE_ERR_INVALID_ARG;
   if (grad_overlaps(grad_logits, T, E, k, logits, nullptr, nullptr, nullptr, token_mask,
                     expert_counts, token_count, grad_loss))
@@ -567,8 +573,8 @@ int moe_router_backward(const float* logits, const int32_t* topk_ids, const floa
       !grad_loss || !grad_logits)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
-      !aligned16(grad_weights) || !aligned16(token_mask) || !aligned16(expert_counts) ||
-      !aligned16(token_count) || !aligned16(grad_loss) || !aligned16(grad_logits))
+      !aligned16(grad_weights) || !aligned16(token_mask) || !aligned_experts(expert_counts, E) ||
+      !aligned4(token_count) || !aligned4(grad_loss) || !aligned16(grad_logits))
     return MOE_ERR_INVALID_ARG;
   if (grad_overlaps(grad_logits, T, E, k, logits, topk_ids, topk_weights, grad_weights, token_mask,
                     expert_counts, token_count, grad_loss))
