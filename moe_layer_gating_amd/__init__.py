@@ -26,8 +26,13 @@ LIB_PATH = os.path.join(_HERE, "libmoe_gfx950.so")
 _lib = None
 
 
+def _public_raw_stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
 _current_device = torch.cuda.current_device
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# the stream's address without a Stream object around it, where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
 
 
 class MoeError(RuntimeError):
