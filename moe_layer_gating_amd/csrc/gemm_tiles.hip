@@ -529,13 +529,11 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
 #define MOE_W2_TILES(MODE_, BM_, YB_)                                                           \
   launch_tiles_w2_mode<MODE_, BM_, YB_>(max_tiles, bb, ww, w2_scale, tiles, num_tiles, H, I,    \
                                         act_amax_bits, y, e0, e1, st)
-  if (mode == MOE_INT8 && !y_bf16)
+  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
+  if (mode == MOE_INT8)
     return launch_w2_large_i8(bm, b, w2, w2_scale, tiles, num_tiles, max_tiles, H, I,
                               reinterpret_cast<const float*>(act_amax_bits),
                               reinterpret_cast<float*>(y), e0, e1, st);
-  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
-  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
-  if (y_bf16 && mode != MOE_FP8_E4M3) return hipErrorInvalidValue;
   if (mode == MOE_BF16 && bm == 64)
     MOE_W2_TILES(MOE_BF16, 64, false);
   else if (mode == MOE_BF16 && bm == 128)

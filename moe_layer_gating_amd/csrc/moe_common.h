@@ -332,8 +332,8 @@ hipError_t launch_w2_tiles(int mode, int bm, const void* b, const void* w2, cons
                            const Tile* tiles, const int32_t* num_tiles, int max_tiles, int H,
                            int I, const uint32_t* act_amax_bits, void* y, bool y_bf16,
                            hipEvent_t e0, hipEvent_t e1, hipStream_t st);
-// The INT8 kernels of the largest tiles (256 positions, gemm_i8_large.hip);
-// xs / hs hold the fp32 scale per token / per sorted position.
+// The tiled INT8 kernels (gemm_i8_large.hip), bm = 64 or 256 positions; xs / hs
+// hold the fp32 scale per token / per sorted position.
 hipError_t launch_w13_large_i8(int bm, const void* b, const void* w13, const float* w13_scale,
                                const int32_t* sorted_ids, const Tile* tiles,
                                const int32_t* num_tiles, int max_tiles, int H, int I, int k,
