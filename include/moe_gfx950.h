@@ -25,7 +25,8 @@
  *    valid sizes) returns MOE_OK at once: no buffer is checked or touched.
  *  - Limits: 1 <= E <= 1024, 1 <= k <= min(E, 16), 0 <= T, T*k < 2^31,
  *    H and I positive multiples of 128 (MOE_ERR_UNSUPPORTED otherwise),
- *    every device pointer 16-byte aligned.
+ *    every device pointer 16-byte aligned (the router's loss and gradients
+ *    name a few that need 4 bytes only).
  *  - Preconditions the device does not check (violations are undefined,
  *    except that a NaN logit is read as -inf, which keeps every expert id in
  *    range): logits hold no NaN and at least k non-(-inf) entries per row;

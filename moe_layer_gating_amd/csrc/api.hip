@@ -60,7 +60,9 @@ struct Layout {
 // INT8: from 8 pairs per expert on, where the small tiles' gate/up blocks fill
 // the chip twice (or from 64 on): 64 experts of H = I = 4096 took, few-token
 // against tiled, 362 / 384 us (gate/up) at 4 pairs each, 407 / 389 at 8, 474 /
-// 394 at 12; one expert of 32 pairs 21 / 32 us.
+// 394 at 12; one expert of 32 pairs 21 / 32 us.  The down projection follows
+// the same choice, also where it is called alone; its blocks follow H, and the
+// two were compared at H = I only.
 inline bool use_tiles(const moe_shape& s) {
   const long np = (long)s.T * s.k;
   if (s.wdtype == MOE_INT8)
@@ -72,7 +74,8 @@ inline bool use_tiles(const moe_shape& s) {
 // gate/up blocks; below that 64-position tiles on half the rows, whose blocks
 // are an eighth.  Measured, both projections of one expert: 4096 pairs at H =
 // I = 4096 (544 blocks of the large tiles) 467 us in the small tiles against
-// 217 us; 1024 pairs at 2048 (80 blocks) 47 against 77 us.
+// 217 us; 1024 pairs at 2048 (80 blocks) 47 against 77 us.  One choice for both
+// projections, compared at H = I only.
 inline int tiles_bm(const moe_shape& s) {
   const long np = (long)s.T * s.k;
   if (s.wdtype == MOE_INT8)

@@ -18,17 +18,16 @@
 // fragments are read under this step's MFMAs, and the one barrier of a stage
 // sits a K step before its end, with 16 MFMAs still to issue behind it.
 //
-// Measured (one card; large_i8 kernel alone): 8 experts of 2048 pairs, 28672 x
-// 4096 gate/up (3.85 Tops) 1.77 ms, 2.17 Pop/s; a square library product of the
-// same type (16384 x 16384 x 8192) reaches 2.13 Pop/s on that card.  Bound by the
-// matrix units at the clock the power limit leaves: without the epilogue 5%
-// less, without loads in the loop 22% less, with all loads from L2 9% less.
-// 4096 tokens on 256 experts (H 7168, I 2048): gate/up 1.63 ms, down 0.93 ms,
-// bound by the memory system: 7.5 and 3.8 GB of weights (1.19 and 0.60 ms at
-// 6.3 TB/s) become 9.9 and 4.8 GB into the L2s, since each XCD reads a tile's
-// rows; without MFMAs 1.5% less, without token loads 8% less, without the output
-// 2% (gate/up) and 16% (down) less.  The register-ring tiles of gemm_tiles.hip,
-// given int8 operands, took 2.55, 1.88 and 1.11 ms for the three.
+// Measured (the kernel alone, mean of 24 calls on two sets of operands, the
+// fastest in brackets): 8 experts of 2048 pairs, 28672 x 4096 gate/up (3.85 Tops)
+// 1.84 ms (1.75), 2.09 Pop/s; a square library product of the same type (16384 x
+// 16384 x 8192) reaches 2.13 Pop/s on one such card: bound by the matrix units at
+// the clock the power limit leaves.  4096 tokens on 256 experts (H 7168, I 2048):
+// gate/up 1.66 ms (1.62), down 1.03 ms (1.01), bound by the memory system: 7.5
+// and 3.8 GB of weights (1.19 and 0.60 ms at 6.3 TB/s) become 9.9 and 4.9 GB into
+// the L2s, since each XCD reads a tile's rows, and the down projection writes
+// 0.94 GB.  The register-ring tiles of gemm_tiles.hip, given int8 operands, took
+// 2.55 ms for the first and 1.88 ms for the second gate/up.
 #include <type_traits>
 
 #include "moe_common.h"
@@ -271,6 +270,8 @@ __device__ __forceinline__ void w13_large_tile(const char* b, const char* w13,
       const f32x4 ws = *reinterpret_cast<const f32x4*>(&L.ws[r]);
 #pragma unroll
       for (int j = 0; j < S::CT; j++) {
+        // 2^x and the reciprocal of the hardware, a few fp32 steps off: h rounds
+        // to bf16, 2^16 times coarser, right after; past -g = 126 ln 2 it may be 0
         float hv[2];
 #pragma unroll
         for (int u = 0; u < 2; u++) {
@@ -373,10 +374,10 @@ __device__ __forceinline__ void w2_large_tile(const char* b, const char* w2, con
 // (a tile's blocks are dealt over the XCDs, so that each L2 holds a share of
 // the expert's weights for the expert's next tile); the 64-position tiles, of
 // experts that mostly have one, are dealt to the XCDs in contiguous eighths
-// instead, which reads a tile's rows into one L2.  Measured, list order
-// against eighths: 4096 tokens on 256 experts 2.81 / 2.86 ms a layer, 8 experts
-// of 2048 pairs 1.89 / 2.32 ms, down projection of 32 pairs per expert 0.688 /
-// 0.667 ms.
+// instead, which reads a tile's rows into one L2.  Measured when it was
+// chosen, list order against eighths: 4096 tokens on 256 experts 2.81 / 2.86 ms
+// a layer (y in bf16 then), 8 experts of 2048 pairs 1.89 / 2.32 ms, down
+// projection of 32 pairs per expert 0.688 / 0.667 ms.
 template <int BM>
 __device__ __forceinline__ bool large_work(const Tile* tiles, const int32_t* num_tiles, int n_blk,
                                            Tile* tl, int* nb) {

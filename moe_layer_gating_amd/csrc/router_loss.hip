@@ -18,8 +18,10 @@
 // large batches (131072 x 256 in a training step: loss 43 us, without its
 // arithmetic 38, since the step's last gradient is still being written back; its
 // gradient 42 us, 6.4 TB/s; 65536 x 256, a third of it padding, both gradients
-// with plain softmax 27 us, 4.4 TB/s), by launch latency for small ones (16 x 64: 3.7 and 2.4 us of
-// kernel under 7 us of host work per call).  L = 16 lanes hold a row of
+// with plain softmax 26 us, 4.6 TB/s), by launch latency for small ones (16 x 64:
+// 3.8 and 2.5 us of kernel under 7 us of host work per call; 4096 x 256: 6.5, 4.2
+// and 5.4 us in three dependent launches for 4 MB).  Blocks of 1024 threads take
+// 64 rows at a time there, so 4096 rows fill 64 of the 256 CUs.  L = 16 lanes hold a row of
 // up to 256 logits (four rows per wave), each lane NC runs of 4 values, so the
 // row reductions stay inside the 16-lane rows that DPP moves reach at full
 // rate; longer rows take 32 or 64 lanes rather than more registers per lane
