@@ -1,5 +1,5 @@
-"""Where the router gradients may write: grad_logits that shares a byte with an
-input is refused.  CPU only: no call here reaches a launch."""
+"""What the router gradients refuse: grad_logits that shares a byte with an
+input, null and misaligned pointers.  CPU only: no call here reaches a launch."""
 import ctypes
 
 import pytest
@@ -39,3 +39,16 @@ def test_a_gradient_over_its_input_is_refused(which, name):
         assert _call(which, {name: a}) == -1, hex(a)
     last = (SIZES[name] - 1) // 16 * 16
     assert _call(which, {name: OUT - last}) == -1
+
+
+@pytest.mark.parametrize("which,name", [(w, n) for w, names in READS.items() for n in names])
+def test_null_and_misaligned_inputs_are_refused(which, name):
+    """With every argument at an address of its own.  E = 8: counts are read 16
+    bytes at a time; the one-word values need 4 bytes."""
+    at = 0x2000000 + 0x10000 * list(SIZES).index(name)
+    if name != "mask":
+        assert _call(which, {name: None}) == -1
+    for off in (1, 2) if name in ("tokens", "grad_loss") else (1, 4, 8):
+        assert _call(which, {name: at + off}) == -1, off
+    for out in (None, OUT + 4, OUT + 8):
+        assert _call(which, {}, out) == -1
